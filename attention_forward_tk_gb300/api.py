@@ -16,6 +16,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libtk_attn.so")
@@ -27,6 +28,7 @@ TK_ATTN_ERR_ARCH = -3
 TK_ATTN_ERR_LAUNCH = -4
 TK_ATTN_ERR_DEVICE_TIMEOUT = -5
 TK_ATTN_ERR_TOO_LARGE = -6
+TK_ATTN_ERR_BAD_INDEX = -7
 
 # every symbol include/tk_attn.h declares
 EXPORTED = (
@@ -51,6 +53,18 @@ EXPORTED = (
     "tk_based_fwd",
     "tk_based_fwd_linear",
     "tk_based_check_args",
+    "tk_attn_qk_norm_rope",
+    "tk_attn_qk_norm_rope_check_args",
+    "tk_attn_qk_norm_rope_bwd",
+    "tk_attn_qk_norm_rope_bwd_workspace_bytes",
+    "tk_attn_qk_norm_rope_bwd_check_args",
+    "tk_attn_kv8_write",
+    "tk_attn_kv8_write_check_args",
+    "tk_attn_kv8_read",
+    "tk_attn_kv8_read_check_args",
+    "tk_attn_fwd_kv8",
+    "tk_attn_fwd_kv8_workspace_bytes",
+    "tk_attn_fwd_kv8_check_args",
 )
 
 
@@ -129,6 +143,37 @@ def library() -> ctypes.CDLL:
         lib.tk_gemm_bf16.argtypes = [vp, vp, vp, i, i, i, vp]
         lib.tk_gemm_bf16_check_args.restype = i
         lib.tk_gemm_bf16_check_args.argtypes = [vp, vp, vp, i, i, i]
+        sz, ll3 = ctypes.c_size_t, ctypes.POINTER(ctypes.c_longlong)
+        norm_in = [vp, ll3, vp, ll3, vp, vp, i, vp, vp]
+        dims = [i, i, i, i, i, i, i, f]  # B, H, Hk, N, D, rot, interleaved, eps
+        lib.tk_attn_qk_norm_rope.restype = i
+        lib.tk_attn_qk_norm_rope.argtypes = norm_in + [vp, vp] + dims + [vp]
+        lib.tk_attn_qk_norm_rope_check_args.restype = i
+        lib.tk_attn_qk_norm_rope_check_args.argtypes = norm_in + [vp, vp] + dims
+        grads = [vp, ll3, vp, ll3, vp, ll3, vp, ll3, vp, vp]
+        lib.tk_attn_qk_norm_rope_bwd.restype = i
+        lib.tk_attn_qk_norm_rope_bwd.argtypes = norm_in + grads + dims + [vp, sz, vp]
+        lib.tk_attn_qk_norm_rope_bwd_check_args.restype = i
+        lib.tk_attn_qk_norm_rope_bwd_check_args.argtypes = norm_in + grads + dims + [vp, sz]
+        lib.tk_attn_qk_norm_rope_bwd_workspace_bytes.restype = sz
+        lib.tk_attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i]
+        write = [vp, ll3, vp, ll3, vp, vp, vp, vp, vp, vp, vp] + [i] * 8
+        lib.tk_attn_kv8_write.restype = i
+        lib.tk_attn_kv8_write.argtypes = write + [vp]
+        lib.tk_attn_kv8_write_check_args.restype = i
+        lib.tk_attn_kv8_write_check_args.argtypes = write
+        read = [vp] * 8 + [i] * 8
+        lib.tk_attn_kv8_read.restype = i
+        lib.tk_attn_kv8_read.argtypes = read + [vp]
+        lib.tk_attn_kv8_read_check_args.restype = i
+        lib.tk_attn_kv8_read_check_args.argtypes = read
+        attend = [vp] * 10 + [i] * 9 + [f, i, vp, sz]
+        lib.tk_attn_fwd_kv8.restype = i
+        lib.tk_attn_fwd_kv8.argtypes = attend + [vp]
+        lib.tk_attn_fwd_kv8_check_args.restype = i
+        lib.tk_attn_fwd_kv8_check_args.argtypes = attend
+        lib.tk_attn_fwd_kv8_workspace_bytes.restype = sz
+        lib.tk_attn_fwd_kv8_workspace_bytes.argtypes = [i] * 5
         _lib = lib
         return _lib
 
@@ -258,6 +303,120 @@ def tk_gemm_bf16(a: int, b: int, c: int, M: int, N: int, K: int, stream: int) ->
 
 def tk_gemm_bf16_check_args(a: int, b: int, c: int, M: int, N: int, K: int) -> int:
     return int(library().tk_gemm_bf16_check_args(a, b, c, M, N, K))
+
+
+def _ll3(strides):
+    """Element strides of batch, head and token as the C calls take them."""
+    return (ctypes.c_longlong * 3)(*strides)
+
+
+def tk_attn_qk_norm_rope(q: int, q_strides, k: int, k_strides, q_weight: int, k_weight: int,
+                         weight_f32: int, turns: int, positions: int, q_out: int, k_out: int,
+                         B: int, H: int, Hk: int, N: int, D: int, rot: int, interleaved: int,
+                         eps: float, stream: int) -> int:
+    return library().tk_attn_qk_norm_rope(q, _ll3(q_strides), k, _ll3(k_strides), q_weight,
+                                          k_weight, weight_f32, turns, positions, q_out, k_out, B,
+                                          H, Hk, N, D, rot, interleaved, eps, stream)
+
+
+def tk_attn_qk_norm_rope_check_args(q: int, q_strides, k: int, k_strides, q_weight: int,
+                                    k_weight: int, weight_f32: int, turns: int, positions: int,
+                                    q_out: int, k_out: int, B: int, H: int, Hk: int, N: int,
+                                    D: int, rot: int, interleaved: int, eps: float) -> int:
+    return library().tk_attn_qk_norm_rope_check_args(
+        q, _ll3(q_strides), k, _ll3(k_strides), q_weight, k_weight, weight_f32, turns, positions,
+        q_out, k_out, B, H, Hk, N, D, rot, interleaved, eps)
+
+
+def tk_attn_qk_norm_rope_bwd(q: int, q_strides, k: int, k_strides, q_weight: int, k_weight: int,
+                             weight_f32: int, turns: int, positions: int, dq_out: int,
+                             dq_out_strides, dk_out: int, dk_out_strides, dq: int, dq_strides,
+                             dk: int, dk_strides, dq_weight: int, dk_weight: int, B: int, H: int,
+                             Hk: int, N: int, D: int, rot: int, interleaved: int, eps: float,
+                             workspace: int, workspace_bytes: int, stream: int) -> int:
+    return library().tk_attn_qk_norm_rope_bwd(
+        q, _ll3(q_strides), k, _ll3(k_strides), q_weight, k_weight, weight_f32, turns, positions,
+        dq_out, _ll3(dq_out_strides), dk_out, _ll3(dk_out_strides), dq, _ll3(dq_strides), dk,
+        _ll3(dk_strides), dq_weight, dk_weight, B, H, Hk, N, D, rot, interleaved, eps, workspace,
+        workspace_bytes, stream)
+
+
+def tk_attn_qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
+    return int(library().tk_attn_qk_norm_rope_bwd_workspace_bytes(D))
+
+
+def tk_attn_qk_norm_rope_bwd_check_args(
+        q: int, q_strides, k: int, k_strides, q_weight: int, k_weight: int, weight_f32: int,
+        turns: int, positions: int, dq_out: int, dq_out_strides, dk_out: int, dk_out_strides,
+        dq: int, dq_strides, dk: int, dk_strides, dq_weight: int, dk_weight: int, B: int, H: int,
+        Hk: int, N: int, D: int, rot: int, interleaved: int, eps: float, workspace: int,
+        workspace_bytes: int) -> int:
+    return library().tk_attn_qk_norm_rope_bwd_check_args(
+        q, _ll3(q_strides), k, _ll3(k_strides), q_weight, k_weight, weight_f32, turns, positions,
+        dq_out, _ll3(dq_out_strides), dk_out, _ll3(dk_out_strides), dq, _ll3(dq_strides), dk,
+        _ll3(dk_strides), dq_weight, dk_weight, B, H, Hk, N, D, rot, interleaved, eps, workspace,
+        workspace_bytes)
+
+
+def tk_attn_kv8_write(k: int, k_strides, v: int, v_strides, k_cache: int, v_cache: int,
+                      k_exp: int, v_exp: int, page_table: int, start: int, counts: int, B: int,
+                      Hkv: int, N: int, D: int, num_pages: int, page: int, max_pages: int,
+                      table_stride: int, stream: int) -> int:
+    return library().tk_attn_kv8_write(k, _ll3(k_strides), v, _ll3(v_strides), k_cache, v_cache,
+                                       k_exp, v_exp, page_table, start, counts, B, Hkv, N, D,
+                                       num_pages, page, max_pages, table_stride, stream)
+
+
+def tk_attn_kv8_write_check_args(k: int, k_strides, v: int, v_strides, k_cache: int, v_cache: int,
+                                 k_exp: int, v_exp: int, page_table: int, start: int, counts: int,
+                                 B: int, Hkv: int, N: int, D: int, num_pages: int, page: int,
+                                 max_pages: int, table_stride: int) -> int:
+    return library().tk_attn_kv8_write_check_args(
+        k, _ll3(k_strides), v, _ll3(v_strides), k_cache, v_cache, k_exp, v_exp, page_table, start,
+        counts, B, Hkv, N, D, num_pages, page, max_pages, table_stride)
+
+
+def tk_attn_kv8_read(k_cache: int, v_cache: int, k_exp: int, v_exp: int, page_table: int,
+                     lengths: int, k: int, v: int, B: int, Hkv: int, N: int, D: int,
+                     num_pages: int, page: int, max_pages: int, table_stride: int,
+                     stream: int) -> int:
+    return library().tk_attn_kv8_read(k_cache, v_cache, k_exp, v_exp, page_table, lengths, k, v,
+                                      B, Hkv, N, D, num_pages, page, max_pages, table_stride,
+                                      stream)
+
+
+def tk_attn_kv8_read_check_args(k_cache: int, v_cache: int, k_exp: int, v_exp: int,
+                                page_table: int, lengths: int, k: int, v: int, B: int, Hkv: int,
+                                N: int, D: int, num_pages: int, page: int, max_pages: int,
+                                table_stride: int) -> int:
+    return library().tk_attn_kv8_read_check_args(
+        k_cache, v_cache, k_exp, v_exp, page_table, lengths, k, v, B, Hkv, N, D, num_pages, page,
+        max_pages, table_stride)
+
+
+def tk_attn_fwd_kv8(q: int, k_cache: int, v_cache: int, k_exp: int, v_exp: int, page_table: int,
+                    lengths: int, counts: int, o: int, lse: int, B: int, H: int, Hkv: int, Nq: int,
+                    D: int, num_pages: int, page: int, max_pages: int, table_stride: int,
+                    scale: float, causal: int, workspace: int, workspace_bytes: int,
+                    stream: int) -> int:
+    return library().tk_attn_fwd_kv8(q, k_cache, v_cache, k_exp, v_exp, page_table, lengths,
+                                     counts, o, lse, B, H, Hkv, Nq, D, num_pages, page, max_pages,
+                                     table_stride, scale, causal, workspace, workspace_bytes,
+                                     stream)
+
+
+def tk_attn_fwd_kv8_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, D: int) -> int:
+    return int(library().tk_attn_fwd_kv8_workspace_bytes(B, H, Hkv, Nq, D))
+
+
+def tk_attn_fwd_kv8_check_args(q: int, k_cache: int, v_cache: int, k_exp: int, v_exp: int,
+                               page_table: int, lengths: int, counts: int, o: int, lse: int,
+                               B: int, H: int, Hkv: int, Nq: int, D: int, num_pages: int,
+                               page: int, max_pages: int, table_stride: int, scale: float,
+                               causal: int, workspace: int, workspace_bytes: int) -> int:
+    return library().tk_attn_fwd_kv8_check_args(
+        q, k_cache, v_cache, k_exp, v_exp, page_table, lengths, counts, o, lse, B, H, Hkv, Nq, D,
+        num_pages, page, max_pages, table_stride, scale, causal, workspace, workspace_bytes)
 
 
 # short aliases
@@ -513,3 +672,361 @@ def attention_forward_host(q, k, v, causal: bool = False, scale: float | None = 
         raise TkAttnError(f"tk_attn_fwd_host: {tk_attn_status_string(st)} ({st})", st)
     s.synchronize()
     return out, lse
+
+
+# ----------------------------------------------------------------- a decoder's serving steps
+
+
+def _launch(t, stream, call):
+    """call(stream handle) with the tensor t's device current, and with `stream`
+    (default: torch's current stream there) current too, so that what torch
+    allocates inside belongs to the stream that uses it."""
+    import torch
+    dev = t.device.index
+    if stream is None and torch.cuda.current_device() == dev:
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        if stream.device != t.device:
+            raise ValueError("the stream is on another device than the tensors")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _raise_status(name: str, status: int):
+    raise TkAttnError(f"{name}: {tk_attn_status_string(status)} ({status})", status)
+
+
+def _want(t, name, dtype, shape, device):
+    """t is a contiguous tensor of this type and shape on this device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or \
+            t.device != device:
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on "
+                         f"{device}, not {str(t.dtype)[6:]} {list(t.shape)} on {t.device}")
+
+
+def _want_rows(t, name, shape, device):
+    """t is a bf16 [B, H, N, D] tensor whose last dimension is contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.stride(3) != 1 or \
+            t.device != device:
+        raise ValueError(f"{name} must be a bfloat16 tensor {list(shape)} with a contiguous last "
+                         f"dimension on {device}, not {str(t.dtype)[6:]} {list(t.shape)} with "
+                         f"strides {list(t.stride())} on {t.device}")
+
+
+def _strides(t):
+    """Element strides of batch, head and token (a dimension of one has none)."""
+    return [s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride())]
+
+
+def rope_turns(rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
+    """The plan of frequencies qk_norm_rope takes: int64 [rot / 2], frequency
+    k (inv_freq[k] radians a position, default base^(-2k / rot)) as a 64-bit
+    fraction of one turn.  Position times it, modulo 2^64, is the exact angle at any
+    position; scaled frequencies (for longer contexts) are given as inv_freq."""
+    import torch
+    if rot < 0 or rot % 8:
+        raise ValueError("rot must be a multiple of 8")
+    freq = [base ** (-2.0 * j / rot) for j in range(rot // 2)] if inv_freq is None else \
+        [float(x) for x in inv_freq]
+    if len(freq) != rot // 2 or not all(math.isfinite(x) for x in freq):
+        raise ValueError("inv_freq must hold rot / 2 finite frequencies")
+    # pi to 60 digits, in integers: every bit of the fraction is right for any double
+    pi, one = 3141592653589793238462643383279502884197169399375105820974944, 10 ** 60
+    turns = []
+    for x in freq:
+        num, den = x.as_integer_ratio()
+        top, bottom = num * one << 64, 2 * den * pi
+        t = ((2 * top + bottom) // (2 * bottom)) % (1 << 64)  # rounded to nearest
+        turns.append(t - (1 << 64) if t >= 1 << 63 else t)
+    return torch.tensor(turns, dtype=torch.int64, device=device)
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, turns, positions):
+    import torch
+    if q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0] or q.shape[2:] != k.shape[2:]:
+        raise ValueError("q must be [B, H, N, D] and k [B, Hk, N, D]")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev = q.device
+    B, H, N, D = q.shape
+    Hk = k.shape[1]
+    _want_rows(q, "q", q.shape, dev)
+    _want_rows(k, "k", k.shape, dev)
+    wt = q_weight.dtype
+    if wt != torch.bfloat16 and wt != torch.float32:
+        raise ValueError("q_weight and k_weight must be bfloat16 or float32")
+    _want(q_weight, "q_weight", wt, (D,), dev)
+    _want(k_weight, "k_weight", wt, (D,), dev)
+    rot = 0
+    if turns is not None:
+        _want(turns, "turns", torch.int64, (turns.numel(),), dev)
+        rot = 2 * turns.numel()
+    if positions is not None:
+        _want(positions, "positions", torch.int32, (B, N), dev)
+    return (q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), q_weight.data_ptr(),
+            k_weight.data_ptr(), int(wt == torch.float32),
+            turns.data_ptr() if rot else 0, positions.data_ptr() if positions is not None else 0,
+            ), (B, H, Hk, N, D, rot)
+
+
+def qk_norm_rope_forward(q, k, q_weight, k_weight, turns, positions=None, eps: float = 1e-6,
+                         interleaved: bool = False, out_q=None, out_k=None, stream=None):
+    """RMS norm of each head's query and key and the position rotation in one
+    pass: (q', k') bf16, contiguous [B, H, N, D] and [B, Hk, N, D], as the attention
+    calls take them, of bf16 CUDA tensors of any strides with a contiguous last
+    dimension (views of a fused projection among them).
+
+    q_weight, k_weight: [D], bf16 or fp32; turns: rope_turns(rot) (None: no
+    rotation); positions: int32 [B, N] (None: token i at i); interleaved: pair
+    neighbours rather than halves.  Enqueued on `stream`; returns immediately.
+    """
+    import torch
+    ins, (B, H, Hk, N, D, rot) = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
+    if out_q is not None:
+        _want(out_q, "out_q", torch.bfloat16, (B, H, N, D), q.device)
+    if out_k is not None:
+        _want(out_k, "out_k", torch.bfloat16, (B, Hk, N, D), q.device)
+
+    def call(s):
+        oq = q.new_empty((B, H, N, D)) if out_q is None else out_q
+        ok = q.new_empty((B, Hk, N, D)) if out_k is None else out_k
+        st = tk_attn_qk_norm_rope(*ins, oq.data_ptr(), ok.data_ptr(), B, H, Hk, N, D, rot,
+                                  int(bool(interleaved)), eps, s)
+        if st != TK_ATTN_OK:
+            _raise_status("tk_attn_qk_norm_rope", st)
+        return oq, ok
+
+    return _launch(q, stream, call)
+
+
+def qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out, dk_out, positions=None,
+                          eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None,
+                          workspace=None, stream=None):
+    """Gradients of qk_norm_rope_forward: (dq, dk) in bf16 with q's and k's
+    shapes (views of one fused gradient may be given), and the weights' (dq_weight,
+    dk_weight) in fp32 [D].  dq_out and dk_out: bf16, last dimension contiguous.
+    Equal calls give equal bits.  Enqueued on `stream`; returns immediately.
+    """
+    import torch
+    ins, (B, H, Hk, N, D, rot) = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
+    for t, name, like in ((dq_out, "dq_out", q), (dk_out, "dk_out", k), (dq, "dq", q),
+                          (dk, "dk", k)):
+        if t is not None:
+            _want_rows(t, name, like.shape, q.device)
+    if workspace is not None and workspace.device != q.device:
+        raise ValueError("the workspace must be on the tensors' device")
+
+    def call(s):
+        gq = torch.empty_like(q) if dq is None else dq
+        gk = torch.empty_like(k) if dk is None else dk
+        gw = torch.empty((2, D), dtype=torch.float32, device=q.device)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(tk_attn_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
+                             device=q.device)
+        st = tk_attn_qk_norm_rope_bwd(
+            *ins, dq_out.data_ptr(), _strides(dq_out), dk_out.data_ptr(),
+            _strides(dk_out), gq.data_ptr(), _strides(gq), gk.data_ptr(), _strides(gk),
+            gw.data_ptr(), gw.data_ptr() + 4 * D, B, H, Hk, N, D, rot, int(bool(interleaved)), eps,
+            ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        if st != TK_ATTN_OK:
+            _raise_status("tk_attn_qk_norm_rope_bwd", st)
+        return gq, gk, gw[0], gw[1]
+
+    return _launch(q, stream, call)
+
+
+_norm_rope_fn = None
+
+
+def _norm_rope_function():
+    """The torch.autograd.Function behind qk_norm_rope(), made on first use."""
+    global _norm_rope_fn
+    if _norm_rope_fn is None:
+        import torch
+
+        class _NormRope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, q_weight, k_weight, turns, positions, eps, interleaved):
+                ctx.save_for_backward(q, k, q_weight, k_weight, turns, positions)
+                ctx.eps, ctx.interleaved = eps, interleaved
+                return qk_norm_rope_forward(q, k, q_weight, k_weight, turns, positions, eps,
+                                            interleaved)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dq_out, dk_out):
+                q, k, q_weight, k_weight, turns, positions = ctx.saved_tensors
+                dq_out, dk_out = (t if t.stride(3) == 1 and all(x % 8 == 0 for x in _strides(t))
+                                  else t.contiguous() for t in (dq_out, dk_out))
+                dq, dk, dqw, dkw = qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out,
+                                                         dk_out, positions, ctx.eps,
+                                                         ctx.interleaved)
+                return (dq, dk, dqw.to(q_weight.dtype), dkw.to(k_weight.dtype), None, None, None,
+                        None)
+
+        _norm_rope_fn = _NormRope
+    return _norm_rope_fn
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, turns, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """Differentiable qk_norm_rope_forward (torch autograd: gradients of q, k
+    and both weights).  Runs on torch's current stream of q's device."""
+    return _norm_rope_function().apply(q, k, q_weight, k_weight, turns, positions, float(eps),
+                                       bool(interleaved))
+
+
+class Kv8Cache(NamedTuple):
+    """The 8-bit paged cache's tensors: codes k, v float8_e4m3fn
+    [num_pages, Hkv, page, D] (page 16, 32, 64 or 128; D 64 or 128) and exponents
+    k_exp, v_exp int8 [num_pages, Hkv]; the value held is code * 2^exponent."""
+    k: "torch.Tensor"  # noqa: F821
+    v: "torch.Tensor"  # noqa: F821
+    k_exp: "torch.Tensor"  # noqa: F821
+    v_exp: "torch.Tensor"  # noqa: F821
+
+
+def kv8_cache(num_pages: int, heads: int, page: int, head_dim: int, device="cuda") -> Kv8Cache:
+    """An empty cache (its contents mean nothing until they are written)."""
+    import torch
+    shape = (num_pages, heads, page, head_dim)
+    return Kv8Cache(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                    torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                    torch.zeros(shape[:2], dtype=torch.int8, device=device),
+                    torch.zeros(shape[:2], dtype=torch.int8, device=device))
+
+
+def _kv8_args(cache, page_table, B):
+    """Checked pointers and sizes of a cache and its page tables."""
+    import torch
+    k, v, ke, ve = cache
+    if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or not k.is_cuda or not k.is_contiguous():
+        raise ValueError("the cache's k must be a contiguous float8_e4m3fn CUDA tensor "
+                         "[num_pages, heads, page, D]")
+    dev, shape = k.device, k.shape
+    _want(v, "the cache's v", torch.float8_e4m3fn, shape, dev)
+    _want(ke, "the cache's k_exp", torch.int8, shape[:2], dev)
+    _want(ve, "the cache's v_exp", torch.int8, shape[:2], dev)
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
+            page_table.stride(1) != 1 or page_table.device != dev:
+        raise ValueError(f"page_table must be an int32 tensor [{B}, pages] with contiguous rows "
+                         f"on {dev}")
+    P, H, page, D = shape
+    # one sequence's table has no row stride of its own
+    stride = max(page_table.stride(0), page_table.shape[1])
+    return (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr(), page_table.data_ptr()), \
+        (P, H, page, D, page_table.shape[1], stride), dev
+
+
+def kv8_write(cache: Kv8Cache, k, v, page_table, start, counts=None, stream=None) -> None:
+    """Append rows to the cache: row i < counts[b] of k and v (bf16
+    [B, Hkv, N, D], last dimension contiguous) goes to position start[b] + i of
+    sequence b, quantised with the scale of its page and head.  start, counts:
+    int32 [B]; page_table: int32 [B, pages].  Enqueued on `stream`; returns
+    immediately."""
+    import torch
+    if k.dim() != 4:
+        raise ValueError("k must be [B, Hkv, N, D]")
+    B, Hk, N, Dk = k.shape
+    ptrs, (P, H, page, D, mp, ts), dev = _kv8_args(cache, page_table, B)
+    _want_rows(k, "k", (B, H, N, D), dev)
+    _want_rows(v, "v", (B, H, N, D), dev)
+    _want(start, "start", torch.int32, (B,), dev)
+    if counts is not None:
+        _want(counts, "counts", torch.int32, (B,), dev)
+
+    def call(s):
+        st = tk_attn_kv8_write(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), *ptrs,
+                               start.data_ptr(), counts.data_ptr() if counts is not None else 0, B,
+                               H, N, D, P, page, mp, ts, s)
+        if st != TK_ATTN_OK:
+            _raise_status("tk_attn_kv8_write", st)
+
+    _launch(k, stream, call)
+
+
+def kv8_read(cache: Kv8Cache, page_table, lengths, n: int | None = None, out_k=None, out_v=None,
+             stream=None):
+    """The cache's first min(n, lengths[b]) positions of every sequence in bf16
+    (exact): (k, v), contiguous [B, Hkv, n, D], as the dense attention calls take
+    them.  Rows past a sequence's length are left as they were (zero where this
+    allocates).  n defaults to out_k's, and must be given without out_k and out_v.
+    Enqueued on `stream`; returns immediately."""
+    import torch
+    B = page_table.shape[0] if page_table.dim() == 2 else -1
+    ptrs, (P, H, page, D, mp, ts), dev = _kv8_args(cache, page_table, B)
+    _want(lengths, "lengths", torch.int32, (B,), dev)
+    if n is None:
+        given = out_k if out_k is not None else out_v
+        if given is None:
+            raise ValueError("give n, or out_k and out_v")
+        n = int(given.shape[2]) if given.dim() == 4 else -1
+    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+        if t is not None:
+            _want(t, name, torch.bfloat16, (B, H, n, D), dev)
+
+    def call(s):
+        ok, ov = (torch.zeros((B, H, n, D), dtype=torch.bfloat16, device=dev) if t is None else t
+                  for t in (out_k, out_v))
+        st = tk_attn_kv8_read(*ptrs, lengths.data_ptr(), ok.data_ptr(), ov.data_ptr(), B, H, n, D,
+                              P, page, mp, ts, s)
+        if st != TK_ATTN_OK:
+            _raise_status("tk_attn_kv8_read", st)
+        return ok, ov
+
+    return _launch(cache.k, stream, call)
+
+
+def attention_forward_kv8(q, cache: Kv8Cache, page_table, lengths, counts=None,
+                          causal: bool = True, scale: float | None = None, out=None, lse=None,
+                          workspace=None, stream=None):
+    """O, LSE of bf16 CUDA queries [B, H, Nq, D] (contiguous) against the
+    8-bit paged cache: decode (Nq = 1), drafted tokens and prefill chunks.  Query
+    head h reads key/value head h / (H / Hkv).  lengths: int32 [B], positions in the cache
+    with the queries' own; counts: int32 [B], query rows of each sequence (None:
+    Nq); rows past them are left as they were (unset where this allocates).
+    causal: position j visible to query i iff j <= i + lengths[b] - counts[b].
+    A row that sees nothing gets O = 0 and LSE = -inf.  Outputs and the workspace
+    are allocated by torch when not given.  Enqueued on `stream`; returns
+    immediately."""
+    import torch
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [B, H, Nq, D]")
+    B, H, Nq, Dq = q.shape
+    ptrs, (P, Hkv, page, D, mp, ts), dev = _kv8_args(cache, page_table, B)
+    if Dq != D or H % Hkv or q.device != dev:
+        raise ValueError(f"q must have the cache's head dim {D}, a multiple of its {Hkv} heads, "
+                         f"and be on {dev}")
+    _want(lengths, "lengths", torch.int32, (B,), dev)
+    if counts is not None:
+        _want(counts, "counts", torch.int32, (B,), dev)
+    if out is not None:
+        _want(out, "out", torch.bfloat16, q.shape, dev)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (B, H, Nq), dev)
+    if workspace is not None and workspace.device != dev:
+        raise ValueError("the workspace must be on the tensors' device")
+
+    def call(s):
+        o = torch.empty_like(q) if out is None else out
+        ls = torch.empty((B, H, Nq), dtype=torch.float32, device=dev) if lse is None else lse
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(tk_attn_fwd_kv8_workspace_bytes(B, H, Hkv, Nq, D), dtype=torch.uint8,
+                             device=dev)
+        st = tk_attn_fwd_kv8(q.data_ptr(), *ptrs, lengths.data_ptr(),
+                             counts.data_ptr() if counts is not None else 0, o.data_ptr(),
+                             ls.data_ptr(), B, H, Hkv, Nq, D, P, page, mp, ts,
+                             D ** -0.5 if scale is None else scale, int(bool(causal)),
+                             ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        if st != TK_ATTN_OK:
+            _raise_status("tk_attn_fwd_kv8", st)
+        return o, ls
+
+    return _launch(q, stream, call)

@@ -1,6 +1,7 @@
 """Compile the CUDA library in-tree: ``_build/libtk_attn.so`` for sm_103a.
 
-Two translation units (host launcher + kernels; the host-buffer pipeline),
+Four translation units compiled side by side (attention, Based and GEMM; per-head
+norm with rotation; the 8-bit paged cache; the host-buffer pipeline),
 one ``-gencode``; no cmake.
 The same command works on x86_64 and aarch64 hosts.
 """
@@ -16,14 +17,15 @@ CSRC = os.path.join(_HERE, "csrc")
 INCLUDE = os.path.join(_ROOT, "include")
 BUILD_DIR = os.path.join(_HERE, "_build")
 LIB = os.path.join(BUILD_DIR, "libtk_attn.so")
-SOURCES = [os.path.join(CSRC, "tk_attn.cu"), os.path.join(CSRC, "tk_attn_host.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("tk_attn.cu", "tk_norm_rope.cu", "tk_kv8.cu",
+                                            "tk_attn_host.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
     os.path.join(INCLUDE, "tk_attn.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-std=c++17", "-lineinfo",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC", "-shared", "--threads", "4",
     "-I", INCLUDE, "-I", CSRC,
 ]
 

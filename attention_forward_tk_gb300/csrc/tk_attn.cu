@@ -24,6 +24,7 @@
 #include "tk_attn_fwd.cuh"
 #include "tk_based.cuh"
 #include "tk_based_linear.cuh"
+#include "tk_device.h"
 #include "tk_gemm.cuh"
 
 namespace tkattn {
@@ -38,8 +39,6 @@ __device__ int g_dev_error;
 // address: the address comes from cudaGetSymbolAddress at per-device set-up.
 constexpr size_t kStaticScratchBytes = 64ull << 20;
 static __device__ __align__(256) unsigned char g_splitkv_scratch[kStaticScratchBytes];
-
-constexpr int kMaxDevices = 64;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -179,6 +178,20 @@ DeviceState *current_device(int *status) {
   *status = ds.status;
   return ds.status == TK_ATTN_OK ? &ds : nullptr;
 }
+
+}  // namespace
+
+int device_view(DeviceView *out) {
+  int st;
+  DeviceState *ds = current_device(&st);
+  if (!ds) return st;
+  out->index = (int)(ds - g_dev);
+  out->num_sms = ds->num_sms;
+  out->err_word = ds->err_word;
+  return TK_ATTN_OK;
+}
+
+namespace {
 
 EncodeTiledFn encode_fn() {
   std::call_once(g_encode_once, [] {
@@ -984,6 +997,8 @@ extern "C" const char *tk_attn_status_string(int status) {
     case TK_ATTN_ERR_TOO_LARGE:
       return "the split needs more than the 64 MiB static scratch of tk_attn_fwd_splitkv_static "
              "(use fewer key ranges, or tk_attn_fwd_splitkv with a workspace)";
+    case TK_ATTN_ERR_BAD_INDEX:
+      return "a page, length, position or count on the device was out of its range";
     default: return "unknown status";
   }
 }
@@ -1006,7 +1021,7 @@ extern "C" int tk_attn_last_device_error(tk_attn_stream_t stream) {
     if (cudaMemsetAsync(ds->err_word, 0, sizeof(int), s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
       return TK_ATTN_ERR_LAUNCH;
-    return TK_ATTN_ERR_DEVICE_TIMEOUT;
+    return word == kDevErrIndex ? TK_ATTN_ERR_BAD_INDEX : TK_ATTN_ERR_DEVICE_TIMEOUT;
   }
   return TK_ATTN_OK;
 }

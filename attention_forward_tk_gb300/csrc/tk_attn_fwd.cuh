@@ -58,11 +58,9 @@
 #include <type_traits>
 
 #include "sm103_ptx.cuh"
+#include "tk_device.h"
 
 namespace tkattn {
-
-// error codes written to the device error word (host maps them to statuses)
-constexpr int kDevErrTimeout = 1;
 
 struct FwdParams {
   __nv_bfloat16 *o;  // [BH, N, D]

@@ -1,0 +1,330 @@
+// tk_kv8.cu -- host side of the 8-bit paged cache: argument checks and
+// launches of the write, the read-back and the attention over it (the C ABI is
+// in tk_attn.h; the kernels in tk_kv8_copy.cuh and tk_kv8_decode.cuh).
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "tk_attn.h"
+#include "tk_device.h"
+#include "tk_kv8.h"
+#include "tk_kv8_copy.cuh"
+#include "tk_kv8_decode.cuh"
+
+namespace tkattn {
+namespace {
+
+// Kernel attributes, once per device.
+struct Kv8Device {
+  std::once_flag once;
+  bool ok = false;
+};
+Kv8Device g_kv8_dev[kMaxDevices];
+
+int kv8_device(DeviceView *dv) {
+  const int st = device_view(dv);
+  if (st) return st;
+  Kv8Device &d = g_kv8_dev[dv->index];
+  std::call_once(d.once, [&d] {
+    d.ok = cudaFuncSetAttribute(tk_kv8_decode_kernel<64>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                DecCfg<64>::kSmem) == cudaSuccess &&
+           cudaFuncSetAttribute(tk_kv8_decode_kernel<128>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                DecCfg<128>::kSmem) == cudaSuccess;
+  });
+  return d.ok ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+}
+
+int check_geom(const void *k_cache, const void *v_cache, const void *k_exp, const void *v_exp,
+               const int *table, int num_pages, int Hkv, int page, int D, int max_pages,
+               int table_stride) {
+  if (!k_cache || !v_cache || !k_exp || !v_exp || !table) return TK_ATTN_ERR_INVALID_ARG;
+  if (num_pages <= 0 || Hkv <= 0 || max_pages <= 0 || table_stride < max_pages)
+    return TK_ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return TK_ATTN_ERR_UNSUPPORTED;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return TK_ATTN_ERR_UNSUPPORTED;
+  if (((uintptr_t)k_cache | (uintptr_t)v_cache) & 15u || (uintptr_t)table & 3u)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  if ((long long)max_pages * page > 0x7fffffffLL || 2LL * Hkv > 65535)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  return TK_ATTN_OK;
+}
+
+Kv8Geom geom(int num_pages, int Hkv, int page, int D, int max_pages, int table_stride) {
+  return Kv8Geom{num_pages, Hkv, page, D, max_pages, table_stride};
+}
+
+struct Range {
+  const void *p;
+  size_t n;
+};
+
+// No written range may share a byte with another or with one that is read.
+int check_ranges(const Range *out, int n_out, const Range *in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = i + 1; j < n_out; ++j)
+      if (ranges_overlap((uintptr_t)out[i].p, out[i].n, (uintptr_t)out[j].p, out[j].n))
+        return TK_ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < n_in; ++j)
+      if (ranges_overlap((uintptr_t)out[i].p, out[i].n, (uintptr_t)in[j].p, in[j].n))
+        return TK_ATTN_ERR_INVALID_ARG;
+  }
+  return TK_ATTN_OK;
+}
+
+int log2i(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+size_t table_bytes(int B, int max_pages, int table_stride) {
+  return ((size_t)(B - 1) * table_stride + max_pages) * 4;
+}
+
+}  // namespace
+}  // namespace tkattn
+
+using namespace tkattn;
+
+extern "C" int tk_attn_kv8_write_check_args(
+    const void *k, const long long *k_strides, const void *v, const long long *v_strides,
+    const void *k_cache, const void *v_cache, const void *k_exp, const void *v_exp,
+    const int *page_table, const int *start, const int *counts, int B, int Hkv, int N, int D,
+    int num_pages, int page, int max_pages, int table_stride) {
+  if (!k || !v || !k_strides || !v_strides || !start) return TK_ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || N <= 0) return TK_ATTN_ERR_INVALID_ARG;
+  const int st = check_geom(k_cache, v_cache, k_exp, v_exp, page_table, num_pages, Hkv, page, D,
+                            max_pages, table_stride);
+  if (st) return st;
+  if (((uintptr_t)k | (uintptr_t)v) & 15u || ((uintptr_t)start | (uintptr_t)counts) & 3u)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  for (const long long *s : {k_strides, v_strides})
+    for (int i = 0; i < 3; ++i)
+      if (s[i] < 0 || s[i] % 8 || s[i] >= (1LL << 40)) return TK_ATTN_ERR_UNSUPPORTED;
+  if (B > 65535) return TK_ATTN_ERR_UNSUPPORTED;
+  const size_t payload = (size_t)num_pages * Hkv * page * D, exps = (size_t)num_pages * Hkv;
+  auto extent = [&](const long long *s) {
+    return 2 * (size_t)((B - 1) * s[0] + (Hkv - 1) * s[1] + (N - 1) * s[2] + D);
+  };
+  const Range out[4] = {{k_cache, payload}, {v_cache, payload}, {k_exp, exps}, {v_exp, exps}};
+  const Range in[5] = {{k, extent(k_strides)},
+                       {v, extent(v_strides)},
+                       {page_table, table_bytes(B, max_pages, table_stride)},
+                       {start, (size_t)B * 4},
+                       {counts, counts ? (size_t)B * 4 : 0}};
+  return check_ranges(out, 4, in, 5);
+}
+
+extern "C" int tk_attn_kv8_write(const void *k, const long long *k_strides, const void *v,
+                                 const long long *v_strides, void *k_cache, void *v_cache,
+                                 void *k_exp, void *v_exp, const int *page_table, const int *start,
+                                 const int *counts, int B, int Hkv, int N, int D, int num_pages,
+                                 int page, int max_pages, int table_stride,
+                                 tk_attn_stream_t stream) {
+  int st = tk_attn_kv8_write_check_args(k, k_strides, v, v_strides, k_cache, v_cache, k_exp, v_exp,
+                                        page_table, start, counts, B, Hkv, N, D, num_pages, page,
+                                        max_pages, table_stride);
+  if (st) return st;
+  DeviceView dv;
+  if ((st = kv8_device(&dv))) return st;
+  Kv8WriteParams p;
+  p.g = geom(num_pages, Hkv, page, D, max_pages, table_stride);
+  const void *const src[2] = {k, v};
+  const long long *const ss[2] = {k_strides, v_strides};
+  void *const pay[2] = {k_cache, v_cache}, *const ex[2] = {k_exp, v_exp};
+  for (int i = 0; i < 2; ++i) {
+    p.src[i] = static_cast<const __nv_bfloat16 *>(src[i]);
+    p.sb[i] = ss[i][0];
+    p.sh[i] = ss[i][1];
+    p.sn[i] = ss[i][2];
+    p.payload[i] = static_cast<uint8_t *>(pay[i]);
+    p.exps[i] = static_cast<int8_t *>(ex[i]);
+  }
+  p.table = page_table;
+  p.start = start;
+  p.counts = counts;
+  p.B = B;
+  p.N = N;
+  p.err = dv.err_word;
+  const dim3 grid(kv8_span(N, page), 2 * Hkv, B);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 64)
+    tk_kv8_write_kernel<64><<<grid, kKv8Threads, 0, s>>>(p);
+  else
+    tk_kv8_write_kernel<128><<<grid, kKv8Threads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+}
+
+extern "C" int tk_attn_kv8_read_check_args(const void *k_cache, const void *v_cache,
+                                           const void *k_exp, const void *v_exp,
+                                           const int *page_table, const int *lengths,
+                                           const void *k, const void *v, int B, int Hkv, int N,
+                                           int D, int num_pages, int page, int max_pages,
+                                           int table_stride) {
+  if (!lengths || !k || !v || B <= 0 || N <= 0) return TK_ATTN_ERR_INVALID_ARG;
+  const int st = check_geom(k_cache, v_cache, k_exp, v_exp, page_table, num_pages, Hkv, page, D,
+                            max_pages, table_stride);
+  if (st) return st;
+  if (((uintptr_t)k | (uintptr_t)v) & 15u || (uintptr_t)lengths & 3u)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  if (B > 65535) return TK_ATTN_ERR_UNSUPPORTED;
+  const size_t payload = (size_t)num_pages * Hkv * page * D, exps = (size_t)num_pages * Hkv;
+  const size_t dense = (size_t)B * Hkv * N * D * 2;
+  const Range out[2] = {{k, dense}, {v, dense}};
+  const Range in[6] = {{k_cache, payload},
+                       {v_cache, payload},
+                       {k_exp, exps},
+                       {v_exp, exps},
+                       {page_table, table_bytes(B, max_pages, table_stride)},
+                       {lengths, (size_t)B * 4}};
+  return check_ranges(out, 2, in, 6);
+}
+
+extern "C" int tk_attn_kv8_read(const void *k_cache, const void *v_cache, const void *k_exp,
+                                const void *v_exp, const int *page_table, const int *lengths,
+                                void *k, void *v, int B, int Hkv, int N, int D, int num_pages,
+                                int page, int max_pages, int table_stride,
+                                tk_attn_stream_t stream) {
+  int st = tk_attn_kv8_read_check_args(k_cache, v_cache, k_exp, v_exp, page_table, lengths, k, v,
+                                       B, Hkv, N, D, num_pages, page, max_pages, table_stride);
+  if (st) return st;
+  DeviceView dv;
+  if ((st = kv8_device(&dv))) return st;
+  Kv8ReadParams p;
+  p.g = geom(num_pages, Hkv, page, D, max_pages, table_stride);
+  p.payload[0] = static_cast<const uint8_t *>(k_cache);
+  p.payload[1] = static_cast<const uint8_t *>(v_cache);
+  p.exps[0] = static_cast<const int8_t *>(k_exp);
+  p.exps[1] = static_cast<const int8_t *>(v_exp);
+  p.table = page_table;
+  p.lengths = lengths;
+  p.dst[0] = static_cast<__nv_bfloat16 *>(k);
+  p.dst[1] = static_cast<__nv_bfloat16 *>(v);
+  p.B = B;
+  p.N = N;
+  p.err = dv.err_word;
+  const dim3 grid((int)(((long long)N + 63) / 64), 2 * Hkv, B);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 64)
+    tk_kv8_read_kernel<64><<<grid, kKv8Threads, 0, s>>>(p);
+  else
+    tk_kv8_read_kernel<128><<<grid, kKv8Threads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+}
+
+namespace tkattn {
+namespace {
+
+int decode_tiles(int G, int Nq) {
+  return (int)(((long long)Nq * G + kDecRows - 1) / kDecRows);
+}
+int decode_ctas(const DeviceView &dv) { return 2 * dv.num_sms; }
+
+bool sizes_ok(int B, int H, int Hkv, int Nq, int D) {
+  return B > 0 && H > 0 && Hkv > 0 && Nq > 0 && H % Hkv == 0 && (D == 64 || D == 128);
+}
+
+size_t workspace_for(const DeviceView &dv, int D) {
+  return (size_t)decode_ctas(dv) * 2 * kDecRows * (D + 4) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace tkattn
+
+extern "C" size_t tk_attn_fwd_kv8_workspace_bytes(int B, int H, int Hkv, int Nq, int D) {
+  DeviceView dv;
+  if (!sizes_ok(B, H, Hkv, Nq, D) || device_view(&dv)) return 0;
+  return workspace_for(dv, D);
+}
+
+extern "C" int tk_attn_fwd_kv8_check_args(const void *q, const void *k_cache, const void *v_cache,
+                                          const void *k_exp, const void *v_exp,
+                                          const int *page_table, const int *lengths,
+                                          const int *counts, const void *o, const float *lse,
+                                          int B, int H, int Hkv, int Nq, int D, int num_pages,
+                                          int page, int max_pages, int table_stride, float scale,
+                                          int causal, const void *workspace,
+                                          size_t workspace_bytes) {
+  (void)causal;
+  if (!q || !lengths || !o || !lse || !workspace) return TK_ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || H <= 0 || Nq <= 0 || Hkv <= 0 || H % Hkv) return TK_ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return TK_ATTN_ERR_INVALID_ARG;
+  const int st = check_geom(k_cache, v_cache, k_exp, v_exp, page_table, num_pages, Hkv, page, D,
+                            max_pages, table_stride);
+  if (st) return st;
+  if (((uintptr_t)q | (uintptr_t)o | (uintptr_t)lse | (uintptr_t)workspace) & 15u ||
+      ((uintptr_t)lengths | (uintptr_t)counts) & 3u)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  const long long G = H / Hkv;
+  if (B > 65535 || (long long)Nq * G > (1LL << 30) ||
+      (long long)Hkv * (((long long)Nq * G + kDecRows - 1) / kDecRows) > 0x7fffffffLL ||
+      (long long)B * H > 0x7fffffffLL)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  const size_t payload = (size_t)num_pages * Hkv * page * D, exps = (size_t)num_pages * Hkv;
+  const size_t dense = (size_t)B * H * Nq * D * 2;
+  const Range out[3] = {{o, dense}, {lse, (size_t)B * H * Nq * 4}, {workspace, workspace_bytes}};
+  const Range in[8] = {{q, dense},
+                       {k_cache, payload},
+                       {v_cache, payload},
+                       {k_exp, exps},
+                       {v_exp, exps},
+                       {page_table, table_bytes(B, max_pages, table_stride)},
+                       {lengths, (size_t)B * 4},
+                       {counts, counts ? (size_t)B * 4 : 0}};
+  return check_ranges(out, 3, in, 8);
+}
+
+extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v_cache,
+                               const void *k_exp, const void *v_exp, const int *page_table,
+                               const int *lengths, const int *counts, void *o, float *lse, int B,
+                               int H, int Hkv, int Nq, int D, int num_pages, int page,
+                               int max_pages, int table_stride, float scale, int causal,
+                               void *workspace, size_t workspace_bytes, tk_attn_stream_t stream) {
+  int st = tk_attn_fwd_kv8_check_args(q, k_cache, v_cache, k_exp, v_exp, page_table, lengths,
+                                      counts, o, lse, B, H, Hkv, Nq, D, num_pages, page, max_pages,
+                                      table_stride, scale, causal, workspace, workspace_bytes);
+  if (st) return st;
+  DeviceView dv;
+  if ((st = kv8_device(&dv))) return st;
+  if (workspace_bytes < workspace_for(dv, D)) return TK_ATTN_ERR_INVALID_ARG;
+  Kv8AttnParams p;
+  p.g = geom(num_pages, Hkv, page, D, max_pages, table_stride);
+  p.page_log2 = log2i(page);
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.k = static_cast<const uint8_t *>(k_cache);
+  p.v = static_cast<const uint8_t *>(v_cache);
+  p.ke = static_cast<const int8_t *>(k_exp);
+  p.ve = static_cast<const int8_t *>(v_exp);
+  p.table = page_table;
+  p.lengths = lengths;
+  p.counts = counts;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.lse = lse;
+  p.B = B;
+  p.H = H;
+  p.G = H / Hkv;
+  p.Nq = Nq;
+  p.causal = causal != 0;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.row_tiles = decode_tiles(p.G, Nq);
+  p.ctas = decode_ctas(dv);
+  p.err = dv.err_word;
+  p.part = static_cast<float *>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const long long rows = (long long)Nq * p.G;
+  const dim3 mgrid(Hkv * p.row_tiles, B, rows < kDecRows ? (int)rows : kDecRows);
+  if (D == 64) {
+    tk_kv8_decode_kernel<64><<<p.ctas, kDecThreads, DecCfg<64>::kSmem, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return TK_ATTN_ERR_LAUNCH;
+    tk_kv8_merge_kernel<64><<<mgrid, 64, 0, s>>>(p);
+  } else {
+    tk_kv8_decode_kernel<128><<<p.ctas, kDecThreads, DecCfg<128>::kSmem, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return TK_ATTN_ERR_LAUNCH;
+    tk_kv8_merge_kernel<128><<<mgrid, 128, 0, s>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+}

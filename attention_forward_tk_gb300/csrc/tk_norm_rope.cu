@@ -1,0 +1,591 @@
+// tk_norm_rope.cu -- RMS norm of each head's query and key with the position
+// rotation in the same pass, forward and backward.
+//
+// For every head row x (D values) of a token at position p:
+//   n = x * r,  r = (mean(x^2) + eps)^(-1/2);   y = R(p) (n o w)
+// R(p) turns the pairs (a, b) of the row's first `rot` values by the angles
+// p f_k:  (a, b) -> (a cos - b sin, b cos + a sin); pair k is (k, rot/2 + k),
+// or (2k, 2k+1) when interleaved; the values past `rot` pass unturned.
+// Backward, with g = R(p)^T dy:
+//   dx = r (g o w - n mean(g o w o n)),   dw = sum over rows of g o n.
+//
+// Angles: a frequency is given in turns a position as a 64-bit fraction F of
+// one turn, so p F modulo 2^64 is the exact fraction of a turn at any 32-bit
+// position: no reduction, no loss at far positions.  Its top 32 bits, rounded
+// to fp32, go to sincospif.
+//
+// Mapping: D/8 lanes own a head row, eight values each, in two groups of four
+// placed so that a pair's two values sit in one lane (no exchange for the
+// rotation; three or four shuffles for the mean).  A row group keeps one
+// token's sines and cosines for `hpg` consecutive heads; the groups of a block
+// take consecutive tokens, so a block writes runs of consecutive rows of a head-major output.
+// Everything is computed in fp32 and rounded once to bf16.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <utility>
+
+#include "sm103_ptx.cuh"
+#include "tk_attn.h"
+#include "tk_device.h"
+
+namespace tkattn {
+namespace {
+
+constexpr int kNrThreads = 256;
+// Backward: blocks each keep one row of partial weight gradients.
+constexpr int kNrBwdMaxBlocks = 1024;
+
+struct NrTensor {
+  const __nv_bfloat16 *p;
+  long long sb, sh, sn;  // element strides of batch, head, token
+};
+
+struct NrParams {
+  NrTensor x[2];    // queries, keys
+  NrTensor dy[2];   // backward: gradients of the outputs
+  __nv_bfloat16 *y[2];
+  long long yb[2], yh[2], yn[2];  // element strides of the results
+  const void *w[2];
+  int w_f32;
+  const uint64_t *turns;
+  const int *pos;  // [B, N] or null: 0 .. N-1
+  float eps;
+  int B, N, H[2], rot;
+  int hpg;             // heads a row group takes for one token
+  int chunks[2];       // ceil(H / hpg)
+  long long items;     // (chunks[0] + chunks[1]) * token tiles
+  long long tiles;     // ceil(B * N / groups per block)
+  float *dw_part;      // [gridDim.x, 2, D]
+};
+
+// Element index of a lane's two groups of four: pairs (lo + i, hi + i) when the
+// halves are paired, (lo, lo+1), (lo+2, lo+3), (hi, ..) when interleaved or
+// past the rotated values.
+__device__ __forceinline__ void lane_cols(int l, int rot, bool inter, int &lo, int &hi) {
+  if (!inter && l < rot / 8) {
+    lo = 4 * l;
+    hi = rot / 2 + 4 * l;
+  } else {
+    lo = 8 * l;
+    hi = 8 * l + 4;
+  }
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *row, int lo, int hi, uint2 &a,
+                                      uint2 &b) {
+  a = *reinterpret_cast<const uint2 *>(row + lo);
+  b = *reinterpret_cast<const uint2 *>(row + hi);
+}
+
+__device__ __forceinline__ void widen8(uint2 a, uint2 b, float (&v)[8]) {
+  const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *row, int lo, int hi, const float (&v)[8]) {
+  *reinterpret_cast<uint2 *>(row + lo) =
+      make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  *reinterpret_cast<uint2 *>(row + hi) =
+      make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void load_w(const void *w, int f32, int lo, int hi, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = (i < 4 ? lo : hi) + (i & 3);
+    v[i] = f32 ? static_cast<const float *>(w)[c]
+               : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c]);
+  }
+}
+
+// cos and sin of a lane's four pairs at position p.
+__device__ __forceinline__ void lane_angles(const uint64_t *turns, int l, int p, bool on,
+                                            float (&cs)[4], float (&sn)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t frac = (uint64_t)(long long)p * turns[4 * l + i];
+    // signed 32-bit fraction: half turns in [-1, 1)
+    const float half_turns = (float)(int)(frac >> 32) * 4.656612873077393e-10f;  // 2^-31
+    sincospif(half_turns, &sn[i], &cs[i]);
+  }
+}
+
+// Turn the lane's pairs by (cs, sn): kHalf pairs v[i] with v[4 + i], else
+// neighbours.
+template <bool kHalves>
+__device__ __forceinline__ void turn8(float (&v)[8], const float (&cs)[4], const float (&sn)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float &a = v[kHalves ? i : 2 * i];
+    float &b = v[kHalves ? 4 + i : 2 * i + 1];
+    const float x = a, y = b;
+    a = x * cs[i] - y * sn[i];
+    b = y * cs[i] + x * sn[i];
+  }
+}
+
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float s) {
+#pragma unroll
+  for (int d = kLanes / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s;
+}
+
+// One item = one token tile (a token for each row group of the block) x one
+// run of hpg heads of the queries or the keys.
+template <int D, bool kHalves, bool kBwd>
+__global__ void __launch_bounds__(kNrThreads)
+    tk_norm_rope_kernel(const __grid_constant__ NrParams p) {
+  constexpr int kLanes = D / 8;
+  constexpr int kGroups = kNrThreads / kLanes;
+  constexpr int kUnroll = kBwd ? 2 : 4;  // heads whose rows are loaded together
+  const int l = threadIdx.x % kLanes;
+  const int grp = threadIdx.x / kLanes;
+  int lo, hi;
+  lane_cols(l, p.rot, !kHalves, lo, hi);
+  const bool turned = 8 * l < p.rot;
+  float dw[2][8];
+  if constexpr (kBwd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+  }
+  const long long tokens = (long long)p.B * p.N;
+  for (long long it = blockIdx.x; it < p.items; it += gridDim.x) {
+    const int nchunk = p.chunks[0] + p.chunks[1];
+    const long long tile = it / nchunk;
+    int ch = (int)(it - tile * nchunk);
+    const int which = ch >= p.chunks[0];
+    if (which) ch -= p.chunks[0];
+    const long long tok = tile * kGroups + grp;
+    const bool live = tok < tokens;
+    const int b = live ? (int)(tok / p.N) : 0;
+    const int n = live ? (int)(tok - (long long)b * p.N) : 0;
+    float cs[4], sn[4];
+    const int pos = p.pos ? p.pos[(long long)b * p.N + n] : n;
+    lane_angles(p.turns, l, pos, turned, cs, sn);
+    if constexpr (kBwd) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sn[i] = -sn[i];  // the rotation's transpose
+    }
+    float w[8];
+    load_w(p.w[which], p.w_f32, lo, hi, w);
+    const NrTensor &X = p.x[which];
+    const __nv_bfloat16 *xrow = X.p + b * X.sb + n * X.sn;
+    __nv_bfloat16 *yrow = p.y[which] + b * p.yb[which] + n * p.yn[which];
+    float sum[8];  // backward: this item's g o n
+    if constexpr (kBwd) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    }
+    const int h0 = ch * p.hpg;
+    const int h1 = min(h0 + p.hpg, p.H[which]);
+    for (int h = h0; h < h1; h += kUnroll) {
+      uint2 xa[kUnroll], xb[kUnroll], ga[kUnroll], gb[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        xa[u] = xb[u] = make_uint2(0, 0);
+        if (live && h + u < h1) load8(xrow + (h + u) * X.sh, lo, hi, xa[u], xb[u]);
+        if constexpr (kBwd) {
+          const NrTensor &G = p.dy[which];
+          ga[u] = gb[u] = make_uint2(0, 0);
+          if (live && h + u < h1)
+            load8(G.p + b * G.sb + n * G.sn + (h + u) * G.sh, lo, hi, ga[u], gb[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float v[8];
+        widen8(xa[u], xb[u], v);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+        ss = group_sum<kLanes>(ss);
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const bool store = live && h + u < h1;
+        if constexpr (!kBwd) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
+          if (turned) turn8<kHalves>(v, cs, sn);
+          if (store) store8(yrow + (h + u) * p.yh[which], lo, hi, v);
+        } else {
+          float g[8];
+          widen8(ga[u], gb[u], g);
+          if (turned) turn8<kHalves>(g, cs, sn);
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] *= r;  // n
+            if (store) sum[i] = fmaf(g[i], v[i], sum[i]);
+            g[i] *= w[i];
+            dot = fmaf(g[i], v[i], dot);
+          }
+          dot = group_sum<kLanes>(dot) * (1.f / D);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = r * (g[i] - v[i] * dot);
+          if (store) store8(yrow + (h + u) * p.yh[which], lo, hi, g);
+        }
+      }
+    }
+    if constexpr (kBwd) {
+      if (which) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[1][i] += sum[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[0][i] += sum[i];
+      }
+    }
+  }
+  if constexpr (kBwd) {
+    // the block's sums, in a fixed order
+    __shared__ float part[kGroups][2][D];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = (i < 4 ? lo : hi) + (i & 3);
+      part[grp][0][c] = dw[0][i];
+      part[grp][1][c] = dw[1][i];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kNrThreads) {
+      float s = 0.f;
+      for (int g = 0; g < kGroups; ++g) s += part[g][0][i];
+      p.dw_part[(size_t)blockIdx.x * 2 * D + i] = s;
+    }
+  }
+}
+
+// dw = sum over the blocks' partial rows, in a fixed order: one block for 32
+// columns, 8 warps over the rows, then over the warps.
+__global__ void __launch_bounds__(256)
+    tk_norm_rope_dw_kernel(const float *__restrict__ part, int rows, int D,
+                           float *__restrict__ dqw, float *__restrict__ dkw) {
+  __shared__ float acc[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;  // of 2 D
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  int r = warp;
+  for (; r + 24 < rows; r += 32) {
+    s0 += part[(size_t)r * 2 * D + col];
+    s1 += part[(size_t)(r + 8) * 2 * D + col];
+    s2 += part[(size_t)(r + 16) * 2 * D + col];
+    s3 += part[(size_t)(r + 24) * 2 * D + col];
+  }
+  for (; r < rows; r += 8) s0 += part[(size_t)r * 2 * D + col];
+  acc[warp][lane] = (s0 + s1) + (s2 + s3);
+  __syncthreads();
+  if (warp == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += acc[i][lane];
+    if (col < D)
+      dqw[col] = s;
+    else
+      dkw[col - D] = s;
+  }
+}
+
+bool strides_ok(const long long *s) {
+  for (int i = 0; i < 3; ++i)
+    if (s[i] < 0 || s[i] % 8 || s[i] >= (1LL << 40)) return false;
+  return true;
+}
+
+// Bytes from a tensor's first to past its last element.
+size_t extent(const long long *s, int B, int H, int N, int D) {
+  return 2 * (size_t)((B - 1) * s[0] + (H - 1) * s[1] + (N - 1) * s[2] + D);
+}
+
+// A written tensor must not hold one element twice: every dimension longer
+// than one has to step over the dimensions inside it.
+bool distinct(const long long *s, int B, int H, int N, int D) {
+  struct {
+    long long stride, len;
+  } d[3] = {{s[0], B}, {s[1], H}, {s[2], N}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (d[j].stride < d[i].stride) std::swap(d[i], d[j]);
+  long long inner = D;
+  for (auto &x : d) {
+    if (x.len <= 1) continue;
+    if (x.stride < inner) return false;
+    inner = x.stride * (x.len - 1) + inner;
+  }
+  return true;
+}
+
+// Two written tensors whose extents overlap share no element: both lie in one
+// token-major buffer (the same token and batch strides), their heads in
+// disjoint runs of a token's values.
+bool interleave_apart(uintptr_t a, const long long *sa, int Ha, uintptr_t b, const long long *sb,
+                      int Hb, int B, int N, int D) {
+  if ((b > a ? b - a : a - b) % 2) return false;
+  long long period;  // elements from one token's values to the next's
+  if (N > 1) {
+    period = sa[2];
+    if (sa[2] != sb[2] || period <= 0) return false;
+    if (B > 1 && (sa[0] != sb[0] || sa[0] % period)) return false;
+  } else {
+    period = B > 1 ? sa[0] : 0;
+    if (period <= 0 || sa[0] != sb[0]) return false;
+  }
+  const long long wa = (Ha - 1) * sa[1] + D, wb = (Hb - 1) * sb[1] + D;
+  const long long off = ((long long)b - (long long)a) / 2;
+  const long long r = ((off % period) + period) % period;
+  return r >= wa && r + wb <= period;
+}
+
+struct Call {
+  const void *q, *k, *qw, *kw;
+  const long long *qs, *ks;
+  const unsigned long long *turns;
+  const int *positions;
+  int B, H, Hk, N, D, rot, w_f32;
+  float eps;
+};
+
+int check_common(const Call &c) {
+  if (!c.q || !c.k || !c.qw || !c.kw || !c.qs || !c.ks) return TK_ATTN_ERR_INVALID_ARG;
+  if (c.B <= 0 || c.H <= 0 || c.Hk <= 0 || c.N <= 0 || c.rot < 0 || c.rot > c.D)
+    return TK_ATTN_ERR_INVALID_ARG;
+  if (c.rot > 0 && !c.turns) return TK_ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(c.eps) || c.eps < 0.f) return TK_ATTN_ERR_INVALID_ARG;
+  if ((c.D != 64 && c.D != 128) || c.rot % 8) return TK_ATTN_ERR_UNSUPPORTED;
+  if (((uintptr_t)c.q | (uintptr_t)c.k) & 15u) return TK_ATTN_ERR_UNSUPPORTED;
+  if ((uintptr_t)c.turns & 7u || (uintptr_t)c.positions & 3u ||
+      ((uintptr_t)c.qw | (uintptr_t)c.kw) & (c.w_f32 ? 3u : 1u))
+    return TK_ATTN_ERR_UNSUPPORTED;
+  if (!strides_ok(c.qs) || !strides_ok(c.ks)) return TK_ATTN_ERR_UNSUPPORTED;
+  if ((long long)c.B * c.N > 0x7fffffffLL ||
+      (long long)c.B * c.N * ((long long)c.H + c.Hk) >= (1LL << 40))
+    return TK_ATTN_ERR_UNSUPPORTED;
+  return TK_ATTN_OK;
+}
+
+// Every range of `out` against every other and against the inputs.
+int check_overlap(const uintptr_t *out, const size_t *out_n, int n_out, const uintptr_t *in,
+                  const size_t *in_n, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = i + 1; j < n_out; ++j)
+      if (ranges_overlap(out[i], out_n[i], out[j], out_n[j])) return TK_ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < n_in; ++j)
+      if (ranges_overlap(out[i], out_n[i], in[j], in_n[j])) return TK_ATTN_ERR_INVALID_ARG;
+  }
+  return TK_ATTN_OK;
+}
+
+void fill(NrParams &p, const Call &c) {
+  p.x[0] = {static_cast<const __nv_bfloat16 *>(c.q), c.qs[0], c.qs[1], c.qs[2]};
+  p.x[1] = {static_cast<const __nv_bfloat16 *>(c.k), c.ks[0], c.ks[1], c.ks[2]};
+  p.w[0] = c.qw;
+  p.w[1] = c.kw;
+  p.w_f32 = c.w_f32;
+  p.turns = reinterpret_cast<const uint64_t *>(c.turns);
+  p.pos = c.positions;
+  p.eps = c.eps;
+  p.B = c.B;
+  p.N = c.N;
+  p.H[0] = c.H;
+  p.H[1] = c.Hk;
+  p.rot = c.rot;
+  p.dw_part = nullptr;
+}
+
+// Heads a row group takes for one token: as many as keep every SM busy, up to
+// eight (the sines and cosines are then an eighth of a row's work).
+void split(NrParams &p, int D, int num_sms) {
+  const int groups = kNrThreads / (D / 8);
+  p.tiles = ((long long)p.B * p.N + groups - 1) / groups;
+  int hpg = 8;
+  while (hpg > 1 &&
+         p.tiles * ((p.H[0] + hpg - 1) / hpg + (p.H[1] + hpg - 1) / hpg) < 4LL * num_sms)
+    hpg /= 2;
+  p.hpg = hpg;
+  p.chunks[0] = (p.H[0] + hpg - 1) / hpg;
+  p.chunks[1] = (p.H[1] + hpg - 1) / hpg;
+  p.items = p.tiles * (p.chunks[0] + p.chunks[1]);
+}
+
+template <bool kBwd>
+cudaError_t launch(const NrParams &p, int D, bool halves, int grid, cudaStream_t s) {
+  if (D == 64) {
+    if (halves)
+      tk_norm_rope_kernel<64, true, kBwd><<<grid, kNrThreads, 0, s>>>(p);
+    else
+      tk_norm_rope_kernel<64, false, kBwd><<<grid, kNrThreads, 0, s>>>(p);
+  } else {
+    if (halves)
+      tk_norm_rope_kernel<128, true, kBwd><<<grid, kNrThreads, 0, s>>>(p);
+    else
+      tk_norm_rope_kernel<128, false, kBwd><<<grid, kNrThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace tkattn
+
+using namespace tkattn;
+
+extern "C" int tk_attn_qk_norm_rope_check_args(
+    const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+    const void *q_weight, const void *k_weight, int weight_f32, const unsigned long long *turns,
+    const int *positions, const void *q_out, const void *k_out, int B, int H, int Hk, int N, int D,
+    int rot, int interleaved, float eps) {
+  (void)interleaved;
+  const Call c = {q, k, q_weight, k_weight, q_strides, k_strides, turns, positions,
+                  B, H, Hk, N, D, rot, weight_f32, eps};
+  if (!q_out || !k_out) return TK_ATTN_ERR_INVALID_ARG;
+  int st = check_common(c);
+  if (st) return st;
+  if (((uintptr_t)q_out | (uintptr_t)k_out) & 15u) return TK_ATTN_ERR_UNSUPPORTED;
+  const size_t wb = (size_t)D * (weight_f32 ? 4 : 2);
+  const uintptr_t out[2] = {(uintptr_t)q_out, (uintptr_t)k_out};
+  const size_t out_n[2] = {(size_t)B * H * N * D * 2, (size_t)B * Hk * N * D * 2};
+  const uintptr_t in[6] = {(uintptr_t)q, (uintptr_t)k, (uintptr_t)q_weight, (uintptr_t)k_weight,
+                           (uintptr_t)turns, (uintptr_t)positions};
+  const size_t in_n[6] = {extent(q_strides, B, H, N, D), extent(k_strides, B, Hk, N, D), wb, wb,
+                          (size_t)rot * 4, positions ? (size_t)B * N * 4 : 0};
+  return check_overlap(out, out_n, 2, in, in_n, 6);
+}
+
+extern "C" int tk_attn_qk_norm_rope(
+    const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+    const void *q_weight, const void *k_weight, int weight_f32, const unsigned long long *turns,
+    const int *positions, void *q_out, void *k_out, int B, int H, int Hk, int N, int D, int rot,
+    int interleaved, float eps, tk_attn_stream_t stream) {
+  int st = tk_attn_qk_norm_rope_check_args(q, q_strides, k, k_strides, q_weight, k_weight,
+                                           weight_f32, turns, positions, q_out, k_out, B, H, Hk, N,
+                                           D, rot, interleaved, eps);
+  if (st) return st;
+  DeviceView dv;
+  if ((st = device_view(&dv))) return st;
+  const Call c = {q, k, q_weight, k_weight, q_strides, k_strides, turns, positions,
+                  B, H, Hk, N, D, rot, weight_f32, eps};
+  NrParams p;
+  fill(p, c);
+  void *const outs[2] = {q_out, k_out};
+  for (int i = 0; i < 2; ++i) {
+    p.y[i] = static_cast<__nv_bfloat16 *>(outs[i]);
+    p.yn[i] = D;
+    p.yh[i] = (long long)N * D;
+    p.yb[i] = (long long)p.H[i] * N * D;
+    p.dy[i] = {nullptr, 0, 0, 0};
+  }
+  split(p, D, dv.num_sms);
+  const int grid = (int)(p.items < 0x7fffffffLL ? p.items : 0x7fffffffLL);
+  return launch<false>(p, D, !interleaved, grid, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? TK_ATTN_OK
+             : TK_ATTN_ERR_LAUNCH;
+}
+
+extern "C" size_t tk_attn_qk_norm_rope_bwd_workspace_bytes(int D) {
+  return D == 64 || D == 128 ? (size_t)kNrBwdMaxBlocks * 2 * D * sizeof(float) : 0;
+}
+
+extern "C" int tk_attn_qk_norm_rope_bwd_check_args(
+    const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+    const void *q_weight, const void *k_weight, int weight_f32, const unsigned long long *turns,
+    const int *positions, const void *dq_out, const long long *dq_out_strides, const void *dk_out,
+    const long long *dk_out_strides, const void *dq, const long long *dq_strides, const void *dk,
+    const long long *dk_strides, const float *dq_weight, const float *dk_weight, int B, int H,
+    int Hk, int N, int D, int rot, int interleaved, float eps, const void *workspace,
+    size_t workspace_bytes) {
+  (void)interleaved;
+  const Call c = {q, k, q_weight, k_weight, q_strides, k_strides, turns, positions,
+                  B, H, Hk, N, D, rot, weight_f32, eps};
+  if (!dq_out || !dk_out || !dq || !dk || !dq_weight || !dk_weight || !workspace ||
+      !dq_out_strides || !dk_out_strides || !dq_strides || !dk_strides)
+    return TK_ATTN_ERR_INVALID_ARG;
+  int st = check_common(c);
+  if (st) return st;
+  if (((uintptr_t)dq_out | (uintptr_t)dk_out | (uintptr_t)dq | (uintptr_t)dk |
+       (uintptr_t)workspace) & 15u ||
+      ((uintptr_t)dq_weight | (uintptr_t)dk_weight) & 3u)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  if (!strides_ok(dq_out_strides) || !strides_ok(dk_out_strides) || !strides_ok(dq_strides) ||
+      !strides_ok(dk_strides))
+    return TK_ATTN_ERR_UNSUPPORTED;
+  if (!distinct(dq_strides, B, H, N, D) || !distinct(dk_strides, B, Hk, N, D))
+    return TK_ATTN_ERR_INVALID_ARG;
+  const size_t need = tk_attn_qk_norm_rope_bwd_workspace_bytes(D);
+  if (workspace_bytes < need) return TK_ATTN_ERR_INVALID_ARG;
+  const size_t wb = (size_t)D * (weight_f32 ? 4 : 2);
+  const uintptr_t out[5] = {(uintptr_t)dq, (uintptr_t)dk, (uintptr_t)dq_weight,
+                            (uintptr_t)dk_weight, (uintptr_t)workspace};
+  const size_t out_n[5] = {extent(dq_strides, B, H, N, D), extent(dk_strides, B, Hk, N, D),
+                           (size_t)D * 4, (size_t)D * 4, need};
+  const uintptr_t in[8] = {(uintptr_t)q, (uintptr_t)k, (uintptr_t)q_weight, (uintptr_t)k_weight,
+                           (uintptr_t)turns, (uintptr_t)positions, (uintptr_t)dq_out,
+                           (uintptr_t)dk_out};
+  const size_t in_n[8] = {extent(q_strides, B, H, N, D), extent(k_strides, B, Hk, N, D), wb, wb,
+                          (size_t)rot * 4, positions ? (size_t)B * N * 4 : 0,
+                          extent(dq_out_strides, B, H, N, D), extent(dk_out_strides, B, Hk, N, D)};
+  // dq and dk may lie in one fused gradient, a token's query and key heads in
+  // turn: their extents then overlap, their elements do not.
+  for (int i = 0; i < 5; ++i) {
+    for (int j = i + 1; j < 5; ++j) {
+      if (i == 0 && j == 1 &&
+          interleave_apart(out[0], dq_strides, H, out[1], dk_strides, Hk, B, N, D))
+        continue;
+      if (ranges_overlap(out[i], out_n[i], out[j], out_n[j])) return TK_ATTN_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < 8; ++j)
+      if (ranges_overlap(out[i], out_n[i], in[j], in_n[j])) return TK_ATTN_ERR_INVALID_ARG;
+  }
+  return TK_ATTN_OK;
+}
+
+extern "C" int tk_attn_qk_norm_rope_bwd(
+    const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+    const void *q_weight, const void *k_weight, int weight_f32, const unsigned long long *turns,
+    const int *positions, const void *dq_out, const long long *dq_out_strides, const void *dk_out,
+    const long long *dk_out_strides, void *dq, const long long *dq_strides, void *dk,
+    const long long *dk_strides, float *dq_weight, float *dk_weight, int B, int H, int Hk, int N,
+    int D, int rot, int interleaved, float eps, void *workspace, size_t workspace_bytes,
+    tk_attn_stream_t stream) {
+  int st = tk_attn_qk_norm_rope_bwd_check_args(
+      q, q_strides, k, k_strides, q_weight, k_weight, weight_f32, turns, positions, dq_out,
+      dq_out_strides, dk_out, dk_out_strides, dq, dq_strides, dk, dk_strides, dq_weight, dk_weight,
+      B, H, Hk, N, D, rot, interleaved, eps, workspace, workspace_bytes);
+  if (st) return st;
+  DeviceView dv;
+  if ((st = device_view(&dv))) return st;
+  const Call c = {q, k, q_weight, k_weight, q_strides, k_strides, turns, positions,
+                  B, H, Hk, N, D, rot, weight_f32, eps};
+  NrParams p;
+  fill(p, c);
+  p.y[0] = static_cast<__nv_bfloat16 *>(dq);
+  p.y[1] = static_cast<__nv_bfloat16 *>(dk);
+  const long long *const ys[2] = {dq_strides, dk_strides};
+  for (int i = 0; i < 2; ++i) {
+    p.yb[i] = ys[i][0];
+    p.yh[i] = ys[i][1];
+    p.yn[i] = ys[i][2];
+  }
+  p.dy[0] = {static_cast<const __nv_bfloat16 *>(dq_out), dq_out_strides[0], dq_out_strides[1],
+             dq_out_strides[2]};
+  p.dy[1] = {static_cast<const __nv_bfloat16 *>(dk_out), dk_out_strides[0], dk_out_strides[1],
+             dk_out_strides[2]};
+  split(p, D, dv.num_sms);
+  p.dw_part = static_cast<float *>(workspace);
+  const long long cap = 4LL * dv.num_sms < kNrBwdMaxBlocks ? 4LL * dv.num_sms : kNrBwdMaxBlocks;
+  const int grid = (int)(p.items < cap ? p.items : cap);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch<true>(p, D, !interleaved, grid, s) != cudaSuccess) return TK_ATTN_ERR_LAUNCH;
+  tk_norm_rope_dw_kernel<<<2 * D / 32, 256, 0, s>>>(p.dw_part, grid, D, dq_weight, dk_weight);
+  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+}

@@ -6,7 +6,10 @@
  * tk_attn_fwd_qk and tk_attn_fwd_splitkv_static (queries against a longer
  * key set, keys split into ranges; tk_attn_fwd_qk also causal), tk_attn_bwd
  * (dQ, dK, dV), tk_based_fwd and tk_based_fwd_linear (Based linear attention,
- * direct and linear-time) and tk_gemm_bf16 (C = A B^T), each with argument checks that
+ * direct and linear-time), tk_gemm_bf16 (C = A B^T), and a decoder's serving
+ * steps: tk_attn_qk_norm_rope (and _bwd), the 8-bit paged cache
+ * (tk_attn_kv8_write, tk_attn_kv8_read) and attention over it
+ * (tk_attn_fwd_kv8); each with argument checks that
  * need no GPU, plus status, version and device-error queries.
  *
  * The operation (one call = one whole forward pass over B*H independent
@@ -73,6 +76,9 @@ typedef struct CUstream_st *tk_attn_stream_t;
                                            tk_attn_last_device_error only) */
 #define TK_ATTN_ERR_TOO_LARGE (-6)      /* tk_attn_fwd_splitkv_static: the ranges'
                                            partial results exceed its static scratch */
+#define TK_ATTN_ERR_BAD_INDEX (-7)      /* a page, length, position or count on the device was
+                                           out of its range (reported by
+                                           tk_attn_last_device_error only) */
 
 #define TK_ATTN_VERSION 10600 /* major*10000 + minor*100 + patch */
 
@@ -360,6 +366,199 @@ int tk_gemm_bf16(const void *a, const void *b, void *c, int M, int N, int K,
 /* The argument checks of tk_gemm_bf16 alone (no GPU needed). */
 int tk_gemm_bf16_check_args(const void *a, const void *b, const void *c, int M, int N, int K);
 
+/*
+ * tk_attn_qk_norm_rope -- RMS norm of each head's query and key, and the
+ * position rotation, in one pass over both:
+ *
+ *   n = x r,  r = (mean(x^2) + eps)^(-1/2) over the head's D values
+ *   y = R(p) (n o w)
+ *
+ * R(p) turns pairs (a, b) of the first `rot` values by p f_k:
+ * (a cos - b sin, b cos + a sin); pair k holds values k and rot/2 + k, or with
+ * `interleaved` 2k and 2k + 1.  The values past `rot` are normed, not turned
+ * (rot = 0: the norm alone).
+ *
+ *   q, k        bf16 [B, H, N, D] and [B, Hk, N, D], any strides: *_strides
+ *               holds the element strides of batch, head and token (host
+ *               memory; >= 0, multiples of 8; the D values contiguous), so
+ *               the heads of a fused projection are read where they lie
+ *   q_weight, k_weight   [D], bf16, or fp32 when weight_f32 != 0
+ *   turns       [rot / 2] device, 8-byte aligned: frequency f_k in turns a
+ *               position as a fraction of one turn, round(f_k / (2 pi) 2^64)
+ *               mod 2^64; p times it mod 2^64 is the exact angle at any
+ *               position.  May be NULL when rot == 0.
+ *   positions   int32 [B, N] device, any value; NULL: token i is at i
+ *   q_out, k_out  bf16, contiguous; disjoint from one another and the inputs
+ *   D 64 or 128; rot a multiple of 8 in [0, D]; eps finite and >= 0
+ *
+ * Everything is computed in fp32 and rounded once.  One launch.  Returns as
+ * tk_attn_fwd.  There is no counterpart in the pages: this is the step that
+ * gives tk_attn_fwd and tk_attn_fwd_kv8 their queries and keys in decoders
+ * whose heads are normed.
+ */
+int tk_attn_qk_norm_rope(const void *q, const long long *q_strides, const void *k,
+                         const long long *k_strides, const void *q_weight, const void *k_weight,
+                         int weight_f32, const unsigned long long *turns, const int *positions,
+                         void *q_out, void *k_out, int B, int H, int Hk, int N, int D, int rot,
+                         int interleaved, float eps, tk_attn_stream_t stream);
+
+/* The argument checks of tk_attn_qk_norm_rope alone (no GPU needed). */
+int tk_attn_qk_norm_rope_check_args(const void *q, const long long *q_strides, const void *k,
+                                    const long long *k_strides, const void *q_weight,
+                                    const void *k_weight, int weight_f32,
+                                    const unsigned long long *turns, const int *positions,
+                                    const void *q_out, const void *k_out, int B, int H, int Hk,
+                                    int N, int D, int rot, int interleaved, float eps);
+
+/*
+ * tk_attn_qk_norm_rope_bwd -- gradients of tk_attn_qk_norm_rope.  With
+ * g = R(p)^T dy:  dx = r (g o w - n mean(g o w o n)),
+ * dw = sum over batch, heads and tokens of g o n.
+ *
+ *   q, k, weights, turns, positions, ...  as in the forward call (the norm is
+ *               recomputed from q and k; nothing of the forward is kept)
+ *   dq_out, dk_out   bf16 gradients of q_out, k_out, strided as q and k
+ *   dq, dk      bf16 gradients of q and k, strided; every element distinct.
+ *               They may lie in one fused token-major gradient.
+ *   dq_weight, dk_weight   fp32 [D]
+ *   workspace   device scratch, 16-byte aligned, of at least
+ *               tk_attn_qk_norm_rope_bwd_workspace_bytes(D) bytes; calls that
+ *               share it must not overlap on the GPU
+ *
+ * The weight gradients' sums run in a fixed order: equal calls on one device
+ * give equal bits.  Two launches.
+ */
+int tk_attn_qk_norm_rope_bwd(const void *q, const long long *q_strides, const void *k,
+                             const long long *k_strides, const void *q_weight,
+                             const void *k_weight, int weight_f32,
+                             const unsigned long long *turns, const int *positions,
+                             const void *dq_out, const long long *dq_out_strides,
+                             const void *dk_out, const long long *dk_out_strides, void *dq,
+                             const long long *dq_strides, void *dk, const long long *dk_strides,
+                             float *dq_weight, float *dk_weight, int B, int H, int Hk, int N,
+                             int D, int rot, int interleaved, float eps, void *workspace,
+                             size_t workspace_bytes, tk_attn_stream_t stream);
+
+/* Workspace bytes tk_attn_qk_norm_rope_bwd needs (0 for another D); no GPU needed. */
+size_t tk_attn_qk_norm_rope_bwd_workspace_bytes(int D);
+
+/* The argument checks of tk_attn_qk_norm_rope_bwd alone (no GPU needed). */
+int tk_attn_qk_norm_rope_bwd_check_args(
+    const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+    const void *q_weight, const void *k_weight, int weight_f32, const unsigned long long *turns,
+    const int *positions, const void *dq_out, const long long *dq_out_strides, const void *dk_out,
+    const long long *dk_out_strides, const void *dq, const long long *dq_strides, const void *dk,
+    const long long *dk_strides, const float *dq_weight, const float *dk_weight, int B, int H,
+    int Hk, int N, int D, int rot, int interleaved, float eps, const void *workspace,
+    size_t workspace_bytes);
+
+/*
+ * The 8-bit paged cache (kv8).  Keys and values of many sequences in pages of
+ * `page` consecutive positions (16, 32, 64 or 128):
+ *
+ *   k_cache, v_cache   [num_pages, Hkv, page, D] E4M3 codes, 16-byte aligned
+ *   k_exp, v_exp       [num_pages, Hkv] int8
+ *   page_table         int32 device, B rows of max_pages entries, rows
+ *                      table_stride entries apart; position t of sequence b
+ *                      is row t % page of page page_table[b][t / page]
+ *
+ * The value held is code * 2^exponent.  An exponent is the least
+ * e in [-117, 119] with 448 2^e >= the largest finite magnitude of the rows
+ * (larger magnitudes saturate), so every value held is exact in bf16.
+ * Sequences may share pages that are only read.  Lengths, positions and
+ * tables live on the device, so nothing waits for the host; an entry outside
+ * its range (a page not in [0, num_pages), a length past max_pages * page, a
+ * negative count, ...) is skipped or clamped, never followed, and
+ * tk_attn_last_device_error then returns TK_ATTN_ERR_BAD_INDEX.
+ */
+
+/*
+ * tk_attn_kv8_write -- append rows to the cache: row i < counts[b] of k and v
+ * goes to position start[b] + i of sequence b.
+ *
+ *   k, v        bf16 [B, Hkv, N, D], strided as in tk_attn_qk_norm_rope
+ *   start       int32 [B]; counts int32 [B] in [0, N], or NULL: N each
+ *
+ * A page whose first row is written takes its exponent from the rows written;
+ * a page that keeps rows before the write keeps at least its exponent, and
+ * when the new rows need a larger one the rows kept are rounded again onto it
+ * (exact but at E4M3's subnormal end).  Rows of a page past the last one
+ * written are left as they are, and no longer mean anything if the exponent
+ * changed.  NaN and infinities are held as NaN and do not enter the exponent.
+ * A page written by a call belongs to one sequence of it: two writers of one
+ * page in one call leave its contents unspecified.  One launch.
+ */
+int tk_attn_kv8_write(const void *k, const long long *k_strides, const void *v,
+                      const long long *v_strides, void *k_cache, void *v_cache, void *k_exp,
+                      void *v_exp, const int *page_table, const int *start, const int *counts,
+                      int B, int Hkv, int N, int D, int num_pages, int page, int max_pages,
+                      int table_stride, tk_attn_stream_t stream);
+
+/* The argument checks of tk_attn_kv8_write alone (no GPU needed). */
+int tk_attn_kv8_write_check_args(const void *k, const long long *k_strides, const void *v,
+                                 const long long *v_strides, const void *k_cache,
+                                 const void *v_cache, const void *k_exp, const void *v_exp,
+                                 const int *page_table, const int *start, const int *counts, int B,
+                                 int Hkv, int N, int D, int num_pages, int page, int max_pages,
+                                 int table_stride);
+
+/*
+ * tk_attn_kv8_read -- the cache's first min(N, lengths[b]) positions of every
+ * sequence in bf16 (exact), contiguous [B, Hkv, N, D], as the dense attention
+ * calls take them.  Rows past a sequence's length, or in a page that is out of
+ * range, are left as they were.  One launch.
+ */
+int tk_attn_kv8_read(const void *k_cache, const void *v_cache, const void *k_exp,
+                     const void *v_exp, const int *page_table, const int *lengths, void *k,
+                     void *v, int B, int Hkv, int N, int D, int num_pages, int page,
+                     int max_pages, int table_stride, tk_attn_stream_t stream);
+
+/* The argument checks of tk_attn_kv8_read alone (no GPU needed). */
+int tk_attn_kv8_read_check_args(const void *k_cache, const void *v_cache, const void *k_exp,
+                                const void *v_exp, const int *page_table, const int *lengths,
+                                const void *k, const void *v, int B, int Hkv, int N, int D,
+                                int num_pages, int page, int max_pages, int table_stride);
+
+/*
+ * tk_attn_fwd_kv8 -- attention of Nq query rows a sequence over the cache:
+ * decode (Nq = 1), drafted tokens, prefill chunks, in one call for sequences
+ * of different lengths.  Query head h reads key/value head h / (H / Hkv).
+ *
+ *   q, o        bf16 [B, H, Nq, D];  lse  fp32 [B, H, Nq]
+ *   lengths     int32 [B]: positions in the cache, the queries' own included
+ *   counts      int32 [B] in [0, Nq]: query rows of each sequence, or NULL:
+ *               Nq each.  Rows i >= counts[b] of o and lse are left as they were.
+ *   causal      0: every position below lengths[b] visible; nonzero: position
+ *               j visible to query i iff j <= i + lengths[b] - counts[b] (the
+ *               queries are the last positions)
+ *   scale       finite and > 0
+ *   workspace   device scratch, 16-byte aligned, of at least
+ *               tk_attn_fwd_kv8_workspace_bytes(...) bytes; overwritten; calls
+ *               that share it must not overlap on the GPU
+ *
+ * A row with no visible position gets o = 0 and lse = -inf.  Positions in a
+ * page out of range count as masked.  What lies in masked positions, NaN codes
+ * among it, has no effect.  Returns as tk_attn_fwd_splitkv.
+ */
+int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v_cache, const void *k_exp,
+                    const void *v_exp, const int *page_table, const int *lengths,
+                    const int *counts, void *o, float *lse, int B, int H, int Hkv, int Nq, int D,
+                    int num_pages, int page, int max_pages, int table_stride, float scale,
+                    int causal, void *workspace, size_t workspace_bytes, tk_attn_stream_t stream);
+
+/* Workspace tk_attn_fwd_kv8 needs on the current device (0 for invalid sizes). */
+size_t tk_attn_fwd_kv8_workspace_bytes(int B, int H, int Hkv, int Nq, int D);
+
+/* The argument checks of tk_attn_fwd_kv8 alone, but for the workspace's size
+ * (no GPU needed). */
+int tk_attn_fwd_kv8_check_args(const void *q, const void *k_cache, const void *v_cache,
+                               const void *k_exp, const void *v_exp, const int *page_table,
+                               const int *lengths, const int *counts, const void *o,
+                               const float *lse, int B, int H, int Hkv, int Nq, int D,
+                               int num_pages, int page, int max_pages, int table_stride,
+                               float scale, int causal, const void *workspace,
+                               size_t workspace_bytes);
+
 /* Static, human-readable text for a status code (never NULL). */
 const char *tk_attn_status_string(int status);
 
@@ -370,7 +569,8 @@ int tk_attn_version(void);
  * tk_attn_last_device_error -- synchronises `stream`, then returns and clears
  * the device-side error word of the current device: TK_ATTN_OK, or
  * TK_ATTN_ERR_DEVICE_TIMEOUT if a kernel abandoned a barrier wait (it then
- * stops its work early and its outputs are incomplete), or TK_ATTN_ERR_LAUNCH
+ * stops its work early and its outputs are incomplete), TK_ATTN_ERR_BAD_INDEX
+ * if a kv8 call met an index out of its range, or TK_ATTN_ERR_LAUNCH
  * if the synchronisation itself failed.  Meant for tests and diagnostics.
  */
 int tk_attn_last_device_error(tk_attn_stream_t stream);

@@ -26,6 +26,9 @@ Contents
                    recurrence the kernel examples on the pages use, both in
                    the pages' per-step-renormalising form and in the
                    deferred-division form; tiny sizes only.
+  kv8              (module) the 8-bit paged cache: E4M3 by its bits, writing with a
+                   scale for each page and head, reading back, attention over it
+  norm_rope        (module) per-head RMS norm with rotation, and its gradients
   build            compile the C part (called by the graft entry's build()).
 
 Sources: the attention definition computed by the "RTX 4090 flash attention"
@@ -36,6 +39,7 @@ log over scaled, masked scores).
 """
 from .brute import (attention, attention_qk, attention_qk_rows, attention_rows, build, lib_path,
                     max_threads)
+from . import kv8, norm_rope
 from .backward import attention_bwd
 from .based import based_quadratic, based_recurrent, based_rows
 from .gemm import gemm_abt
@@ -52,7 +56,9 @@ __all__ = [
     "attention_rows",
     "build",
     "gemm_abt",
+    "kv8",
     "lib_path",
     "max_threads",
+    "norm_rope",
     "tiled_online_softmax",
 ]
