@@ -23,17 +23,20 @@ struct Kv8Device {
 };
 Kv8Device g_kv8_dev[kMaxDevices];
 
+template <int D, int kNT>
+bool configure_decode() {
+  return cudaFuncSetAttribute(tk_kv8_decode_kernel<D, kNT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              DecCfg<D, kNT>::kSmem) == cudaSuccess;
+}
+
 int kv8_device(DeviceView *dv) {
   const int st = device_view(dv);
   if (st) return st;
   Kv8Device &d = g_kv8_dev[dv->index];
   std::call_once(d.once, [&d] {
-    d.ok = cudaFuncSetAttribute(tk_kv8_decode_kernel<64>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                DecCfg<64>::kSmem) == cudaSuccess &&
-           cudaFuncSetAttribute(tk_kv8_decode_kernel<128>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                DecCfg<128>::kSmem) == cudaSuccess;
+    d.ok = configure_decode<64, 1>() && configure_decode<64, 2>() && configure_decode<128, 1>() &&
+           configure_decode<128, 2>();
   });
   return d.ok ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }
@@ -48,7 +51,8 @@ int check_geom(const void *k_cache, const void *v_cache, const void *k_exp, cons
   if (page != 16 && page != 32 && page != 64 && page != 128) return TK_ATTN_ERR_UNSUPPORTED;
   if (((uintptr_t)k_cache | (uintptr_t)v_cache) & 15u || (uintptr_t)table & 3u)
     return TK_ATTN_ERR_UNSUPPORTED;
-  if ((long long)max_pages * page > 0x7fffffffLL || 2LL * Hkv > 65535)
+  if ((long long)max_pages * page > 0x7fffffffLL || 2LL * Hkv > 65535 ||
+      (long long)num_pages * Hkv > 0x7fffffffLL)
     return TK_ATTN_ERR_UNSUPPORTED;
   return TK_ATTN_OK;
 }
@@ -219,17 +223,43 @@ extern "C" int tk_attn_kv8_read(const void *k_cache, const void *v_cache, const 
 namespace tkattn {
 namespace {
 
-int decode_tiles(int G, int Nq) {
-  return (int)(((long long)Nq * G + kDecRows - 1) / kDecRows);
+// Query rows of a tile: eight where the call has no more, else sixteen.
+int tile_rows(int G, int Nq) { return (long long)Nq * G <= 8 ? 8 : 16; }
+int row_tiles(int G, int Nq) {
+  const int t = tile_rows(G, Nq);
+  return (int)(((long long)Nq * G + t - 1) / t);
 }
-int decode_ctas(const DeviceView &dv) { return 2 * dv.num_sms; }
+// Runs the work is cut into: the CTAs that fit on the device at once.
+int decode_ctas(const DeviceView &dv, int rows) {
+  return (rows == 8 ? DecCfg<128, 1>::kCtasPerSm : DecCfg<128, 2>::kCtasPerSm) * dv.num_sms;
+}
 
 bool sizes_ok(int B, int H, int Hkv, int Nq, int D) {
   return B > 0 && H > 0 && Hkv > 0 && Nq > 0 && H % Hkv == 0 && (D == 64 || D == 128);
 }
 
-size_t workspace_for(const DeviceView &dv, int D) {
-  return (size_t)decode_ctas(dv) * 2 * kDecRows * (D + 4) * sizeof(float);
+size_t workspace_for(const DeviceView &dv, int G, int Nq, int D) {
+  const int t = tile_rows(G, Nq);
+  return (size_t)decode_ctas(dv, t) * 2 * t * (D + 4) * sizeof(float);
+}
+
+template <int D, int kNT>
+cudaError_t launch_decode(const Kv8AttnParams &p, dim3 merge_grid, cudaStream_t s) {
+  tk_kv8_decode_kernel<D, kNT><<<p.ctas, kDecThreads, DecCfg<D, kNT>::kSmem, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // The merge starts while the runs still work, finds what it has to do, and
+  // waits for them on the device.
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = merge_grid;
+  cfg.blockDim = dim3(D);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tk_kv8_merge_kernel<D>, p);
 }
 
 }  // namespace
@@ -238,7 +268,7 @@ size_t workspace_for(const DeviceView &dv, int D) {
 extern "C" size_t tk_attn_fwd_kv8_workspace_bytes(int B, int H, int Hkv, int Nq, int D) {
   DeviceView dv;
   if (!sizes_ok(B, H, Hkv, Nq, D) || device_view(&dv)) return 0;
-  return workspace_for(dv, D);
+  return workspace_for(dv, H / Hkv, Nq, D);
 }
 
 extern "C" int tk_attn_fwd_kv8_check_args(const void *q, const void *k_cache, const void *v_cache,
@@ -261,7 +291,7 @@ extern "C" int tk_attn_fwd_kv8_check_args(const void *q, const void *k_cache, co
     return TK_ATTN_ERR_UNSUPPORTED;
   const long long G = H / Hkv;
   if (B > 65535 || (long long)Nq * G > (1LL << 30) ||
-      (long long)Hkv * (((long long)Nq * G + kDecRows - 1) / kDecRows) > 0x7fffffffLL ||
+      (long long)Hkv * (((long long)Nq * G + 7) / 8) > 0x7fffffffLL ||
       (long long)B * H > 0x7fffffffLL)
     return TK_ATTN_ERR_UNSUPPORTED;
   const size_t payload = (size_t)num_pages * Hkv * page * D, exps = (size_t)num_pages * Hkv;
@@ -290,7 +320,7 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
   if (st) return st;
   DeviceView dv;
   if ((st = kv8_device(&dv))) return st;
-  if (workspace_bytes < workspace_for(dv, D)) return TK_ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < workspace_for(dv, H / Hkv, Nq, D)) return TK_ATTN_ERR_INVALID_ARG;
   Kv8AttnParams p;
   p.g = geom(num_pages, Hkv, page, D, max_pages, table_stride);
   p.page_log2 = log2i(page);
@@ -310,21 +340,18 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
   p.Nq = Nq;
   p.causal = causal != 0;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.row_tiles = decode_tiles(p.G, Nq);
-  p.ctas = decode_ctas(dv);
+  p.tile_rows = tile_rows(p.G, Nq);
+  p.row_tiles = row_tiles(p.G, Nq);
+  p.ctas = decode_ctas(dv, p.tile_rows);
   p.err = dv.err_word;
   p.part = static_cast<float *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long rows = (long long)Nq * p.G;
-  const dim3 mgrid(Hkv * p.row_tiles, B, rows < kDecRows ? (int)rows : kDecRows);
-  if (D == 64) {
-    tk_kv8_decode_kernel<64><<<p.ctas, kDecThreads, DecCfg<64>::kSmem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return TK_ATTN_ERR_LAUNCH;
-    tk_kv8_merge_kernel<64><<<mgrid, 64, 0, s>>>(p);
-  } else {
-    tk_kv8_decode_kernel<128><<<p.ctas, kDecThreads, DecCfg<128>::kSmem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return TK_ATTN_ERR_LAUNCH;
-    tk_kv8_merge_kernel<128><<<mgrid, 128, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+  const dim3 merge_grid(Hkv * p.row_tiles, B, rows < p.tile_rows ? (int)rows : p.tile_rows);
+  const bool one = p.tile_rows == 8;
+  const cudaError_t e = D == 64 ? (one ? launch_decode<64, 1>(p, merge_grid, s)
+                                       : launch_decode<64, 2>(p, merge_grid, s))
+                                : (one ? launch_decode<128, 1>(p, merge_grid, s)
+                                       : launch_decode<128, 2>(p, merge_grid, s));
+  return e == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }

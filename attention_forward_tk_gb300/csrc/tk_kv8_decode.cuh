@@ -8,31 +8,40 @@
 // causal mask up to the row's own position).
 //
 // Bound by reading the cache once, so the kernel streams it:
-//  - Work is the list of (sequence, head, 16-row tile, 64-position unit); every
+//  - Work is the list of (sequence, head, row tile, 64-position unit); every
 //    CTA takes an equal run of it, whatever the lengths (they live on the
 //    device; each CTA finds its run by a scan over the sequences).  A run that
 //    starts or ends inside a segment leaves a partial result (running maximum,
 //    sum and unnormalised O in fp32) that a second kernel merges.
-//  - A warp takes 16 positions of each unit.  Every lane copies the bytes it
-//    will use itself with cp.async into its own slots of a ring, so the loop
-//    has no barrier at all.  Which lane takes what is the tensor core's operand
-//    layout: the order of a dot product's terms is free, so a lane's 16
+//  - A warp takes 16 positions of each unit, one run of 16 D bytes of keys and
+//    one of values (a page is a multiple of 16 positions), copied by cp.async
+//    into its own ring: no barrier but the warp's own.  Rows are stored with
+//    their 16-byte pieces exchanged so that the operand loads are free of bank
+//    conflicts.  The order of a dot product's terms is free, so a lane's 16
 //    consecutive bytes of a key row are its operand words of four k-steps; a
-//    lane's 16 consecutive values of four positions are, byte-transposed in
-//    registers, its operand of all PV steps.
-//  - Products are mma.sync m16n8k16 in fp16 with fp32 accumulation: E4M3 is
-//    exact in fp16 and one conversion makes two values.  The tensor rate of
-//    this path is a quarter of what the stream needs at most (16 rows), so the
-//    5th-generation path with its 128-row tiles would gain nothing here.
+//    lane's D/8 consecutive values of four positions are, byte-transposed in
+//    registers, its operand of all PV steps.  (Copies in which a lane fetched
+//    what it would use, half a line a row, brought every line of keys twice
+//    from L2: 5.0 TB/s.)
+//  - Products are mma.sync m16n8k16 in fp16 with fp32 accumulation, positions
+//    (S^T = K Q^T) and value columns (O^T = V^T P^T) on the 16-row side, query
+//    rows on the 8-wide side: E4M3 is exact in fp16, one conversion makes two
+//    values, and eight rows fill a tile.  With the query rows on the 16-row
+//    side the same step took twice the products, exponentials and accumulators:
+//    232 registers, two warps a scheduler, 3.8 TB/s at 8 x 16384 positions of
+//    32 heads.  The 5th-generation path has 128-row tiles, sixteen times the
+//    rows there are.
 //
 // Numbers: q rows are scaled by a power of two to a largest magnitude in
 // [1, 2) before rounding to fp16 (exact but for elements below 2^-14 of the
 // row's largest), the factor returning in the fp32 scores.  m (base 2) is the
-// running maximum of the scores, l = sum 2^(s - m) in fp32.  O is held
-// relative to its own reference M, the running maximum of s + ve, because a
-// page's value exponent multiplies its probabilities: P' = 2^(s + ve - M + 6)
-// <= 2^14 in fp16 keeps 2^-30 of the largest contribution.  Both references
-// move only when exceeded by 2^8, so O is rescaled rarely.
+// running maximum of the scores, moved only when a score exceeds it by 2^8;
+// l = sum 2^(s - m) in fp32.  A page's value exponent multiplies its
+// probabilities, so O is held relative to its own reference M, the running
+// maximum of m + ve: P' = 2^(s + ve - M + 7) <= 2^15 in fp16, whose least value
+// is 2^-31 of a weight 1 in the page of the largest exponent.  While neither
+// reference moves, a step has no exchange between lanes but the operand's
+// transposition and one vote.
 // A NaN code in a masked or stale row must not reach the sums: scores of
 // masked positions are replaced, value rows at or past the length are zeroed,
 // and where rows of one tile see different positions a NaN among those is
@@ -61,7 +70,8 @@ struct Kv8AttnParams {
   int B, H, G, Nq;  // G = H / Hkv
   int causal;
   float scale_log2;  // scale * log2(e)
-  int row_tiles;     // ceil(Nq * G / rows of a tile)
+  int tile_rows;     // query rows of a tile
+  int row_tiles;     // ceil(Nq * G / tile_rows)
   int ctas;          // runs the work is cut into
   int *err;
   float *part;       // [ctas, 2, rows of a tile, D + 4]
@@ -69,21 +79,24 @@ struct Kv8AttnParams {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kDecRows = 16;
 constexpr int kDecUnit = kDecWarps * 16;  // positions of a unit
-constexpr int kDecStages = 4;
-constexpr float kDecTau = 8.f;    // lazy references: exceeded by at most 2^8
-constexpr float kDecLift = 6.f;   // P' is lifted by 2^6
+constexpr float kDecTau = 8.f;       // m is exceeded by at most 2^8
+constexpr float kDecLift = 7.f;      // P' is lifted by 2^7
+constexpr float kDecNone = -1e30f;   // references before any score
 
-template <int D>
+// kNT tiles of eight query rows.
+template <int D, int kNT>
 struct DecCfg {
+  static constexpr int kRows = 8 * kNT;
+  static constexpr int kStages = 3;
   static constexpr int kRun = D / 8;            // output columns of a lane's run
   static constexpr int kRunStride = kRun + 4;   // in the merge buffer (bank spread)
   static constexpr int kRowStride = 8 * kRunStride + 4;
   static constexpr int kStageBytes = 16 * D * 2;  // a warp's keys and values of a unit
-  static constexpr int kRingBytes = kDecWarps * kDecStages * kStageBytes;
-  static constexpr int kMergeBytes = kDecWarps * kDecRows * (kRowStride + 4) * 4;
+  static constexpr int kRingBytes = kDecWarps * kStages * kStageBytes;
+  static constexpr int kMergeBytes = kDecWarps * kRows * (kRowStride + 4) * 4;
   static constexpr int kSmem = kRingBytes + kMergeBytes;
+  static constexpr int kCtasPerSm = kNT == 1 ? 3 : 2;
 };
 
 // A sequence as the kernels use it.
@@ -115,15 +128,15 @@ struct Kv8Place {
   int b;
 };
 
-// Total work, and the sequence in which unit `u` lies (b = B when past the
+// Total work, and the sequence in which run `run` starts (b = B when past the
 // end), or with find_b >= 0 the units before sequence find_b.  Whole block;
 // ends with a barrier.
 __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, int unit, long long segs,
-                                         long long u_mul, int find_b, Kv8Place *out,
-                                         long long *red) {
+                                         int run, int find_b, Kv8Place *out, long long *red) {
   const int nthr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long sum = 0;
-  for (int b = threadIdx.x; b < p.B; b += nthr) sum += seq_units(p, b, unit) * segs;
+  const long long v0 = threadIdx.x < p.B ? seq_units(p, threadIdx.x, unit) * segs : 0;
+  long long sum = v0;
+  for (int b = threadIdx.x + nthr; b < p.B; b += nthr) sum += seq_units(p, b, unit) * segs;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0) red[warp] = sum;
@@ -131,13 +144,13 @@ __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, int unit, long 
   __syncthreads();
   long long total = 0;
   for (int w = 0; w < nthr / 32; ++w) total += red[w];
-  const long long share = max(1LL, (total + p.ctas - 1) / p.ctas);
-  const long long u = u_mul * share;
+  if (threadIdx.x == 0) out->total = total;
+  const long long u = run * max(1LL, (total + p.ctas - 1) / p.ctas);
   __syncthreads();
   long long carry = 0;
   for (int base = 0; base < p.B; base += nthr) {
     const int b = base + threadIdx.x;
-    const long long v = b < p.B ? seq_units(p, b, unit) * segs : 0;
+    const long long v = base == 0 ? v0 : b < p.B ? seq_units(p, b, unit) * segs : 0;
     long long inc = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -148,18 +161,14 @@ __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, int unit, long 
     __syncthreads();
     long long before = carry;
     for (int w = 0; w < warp; ++w) before += red[w];
-    long long all = carry;
-    for (int w = 0; w < nthr / 32; ++w) all += red[w];
+    for (int w = 0; w < nthr / 32; ++w) carry += red[w];
     const long long lo = before + inc - v;
     if (b < p.B && (find_b >= 0 ? b == find_b : (u >= lo && u < lo + v))) {
       out->b = b;
       out->prefix = lo;
     }
-    carry = all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) out->total = total;
-  __syncthreads();
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -173,15 +182,38 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// An 8 x 8 matrix of 16-bit values, one row to four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Four E4M3 codes -> two f16x2 (bytes 0, 1 and 2, 3).
+__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t &a, uint32_t &b) {
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+}
+
+// This launch's dependents may start (they wait before they read); and wait
+// for the launch this one depends on.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Any byte of w an E4M3 NaN (0x7f or 0xff).
@@ -208,15 +240,15 @@ __device__ __forceinline__ void dec_advance(const Kv8AttnParams &p, DecCursor &c
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kDecThreads, 2)
+template <int D, int kNT>
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     tk_kv8_decode_kernel(const __grid_constant__ Kv8AttnParams p) {
-  using C = DecCfg<D>;
-  constexpr int kSteps = D / 16;   // k-steps of Q K^T
+  using C = DecCfg<D, kNT>;
+  constexpr int kStages = C::kStages;
+  constexpr int kSteps = D / 16;   // k-steps of K Q^T, 16-column tiles of O
   constexpr int kChunks = D / 64;  // 16-byte pieces of a key row a lane takes
-  constexpr int kTiles = D / 8;    // 8-column tiles of O
   constexpr int kVw = D / 32;      // words of a value row a lane takes
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Kv8Place place;
   __shared__ long long red[kDecWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,8 +256,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const Kv8Geom &g = p.g;
   const int segs = g.Hkv * p.row_tiles;
   float *merge_o = reinterpret_cast<float *>(smem + C::kRingBytes);
-  float *merge_s = merge_o + kDecWarps * kDecRows * C::kRowStride;  // m, M, l of each warp's rows
+  float *merge_s = merge_o + kDecWarps * C::kRows * C::kRowStride;  // m, M, l of each warp's rows
 
+  grid_launch_dependents();
   if (blockIdx.x == 0) {  // report what is out of range, once
     bool bad = false;
     for (int b = threadIdx.x; b < p.B; b += kDecThreads) {
@@ -252,60 +285,70 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   }
   DecCursor prod = cons;
 
-  const uint32_t ring = smem_addr(smem) + warp * kDecStages * C::kStageBytes;
-  // the page of the step that is issued next: an index, -1 no positions
+  // this lane's places in 16 rows: the copies' destination, and the operand
+  // reads' (rows of 128 bytes: piece ^ row % 8; of 64 bytes: piece ^ row / 2 % 4)
+  uint32_t put, k_get, v_get[2];
+  if constexpr (D == 128) {
+    put = (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 3)) * 16;
+    k_get = q8 * 128 + ((2 * c4) ^ q8) * 16;  // piece 2 c4 + j: ^ 16 j
+    v_get[0] = (2 * c4) * 128 + (q8 ^ (2 * c4)) * 16;
+    v_get[1] = (2 * c4 + 1) * 128 + (q8 ^ (2 * c4 + 1)) * 16;
+  } else {
+    put = (lane >> 2) * 64 + ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
+    k_get = q8 * 64 + (c4 ^ (q8 >> 1)) * 16;
+    v_get[0] = (2 * c4) * 64 + ((q8 >> 1) ^ c4) * 16 + (q8 & 1) * 8;
+    v_get[1] = v_get[0] + 64;
+  }
+  const uint32_t ring = smem_addr(smem) + warp * kStages * C::kStageBytes + put;
+  // the page of the step that is issued next: an index, -2 no positions
   auto fetch_page = [&]() -> int {
     const int t = prod.unit * kDecUnit + warp * 16;
     return t < prod.len ? p.table[kv8_table_offset(g, prod.b, t >> p.page_log2)] : -2;
   };
-  // Copies of one step; the exponents of its page, or bit 16 when there is
+  // Copies of one step; where its page's exponents lie, or -1 when there is
   // nothing to read.
   auto issue = [&](int stage, int id) -> int {
     if (!kv8_page_ok(g, id)) {
       if (id != -2 && lane == 0) atomicCAS(p.err, 0, kDevErrIndex);
       cp_async_commit();
-      return 1 << 16;
+      return -1;
     }
-    const int h = prod.seg / p.row_tiles;
+    const int h = p.row_tiles == 1 ? prod.seg : prod.seg / p.row_tiles;
     const int t = prod.unit * kDecUnit + warp * 16;
-    const long long off = kv8_row_offset(g, id, h, t & (g.page - 1));
-    const uint32_t dst = ring + stage * C::kStageBytes;
+    const int eoff = id * g.Hkv + h;  // (the host bounds num_pages * Hkv)
+    const long long off = (long long)eoff * (g.page * D) + (t & (g.page - 1)) * D;
+    const uint8_t *ks = p.k + off + lane * 16, *vs = p.v + off + lane * 16;
+    const uint32_t dk = ring + stage * C::kStageBytes;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int j = 0; j < kChunks; ++j)
-        cp_async16(dst + ((n * kChunks + j) * 32 + lane) * 16,
-                   p.k + off + (n * 8 + q8) * D + (c4 + 4 * j) * 16);
-    const uint32_t dv = dst + 16 * D;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = 2 * c4 + (i & 1) + (i >> 1) * 8;
-      const uint8_t *src = p.v + off + tok * D + q8 * kVw * 4;
-      if constexpr (D == 128)
-        cp_async16(dv + (i * 32 + lane) * 16, src);
-      else
-        cp_async8(dv + (i * 32 + lane) * 8, src);
+    for (int i = 0; i < D / 32; ++i) {
+      // (D = 128: rows 4 i .., so the exchanged piece alternates)
+      const uint32_t d = D == 128 && (i & 1) ? (dk ^ 64) + i * 512 : dk + i * 512;
+      cp_async16(d, ks + i * 512);
+      cp_async16(d + 16 * D, vs + i * 512);
     }
     cp_async_commit();
-    const long long eoff = kv8_exp_offset(g, id, h);
-    return (int)(uint8_t)p.ke[eoff] | (int)(uint8_t)p.ve[eoff] << 8;
+    return eoff;
   };
 
-  int ex[kDecStages - 1];
+  // Exponents are loaded one step before their use, a step after their page
+  // is known: nothing waits for them.
+  int eo[kStages - 1];
   int next_id = fetch_page();
 #pragma unroll
-  for (int s = 0; s < kDecStages - 1; ++s) {
+  for (int s = 0; s < kStages - 1; ++s) {
     if (s < nsteps) {
-      ex[s] = issue(s, next_id);
+      eo[s] = issue(s, next_id);
       dec_advance(p, prod, segs);
       next_id = s + 1 < nsteps ? fetch_page() : -2;
     } else {
       cp_async_commit();
-      ex[s] = 1 << 16;
+      eo[s] = -1;
     }
   }
+  int eo_now = eo[0];
+  int ke_now = eo_now >= 0 ? p.ke[eo_now] : 0, ve_now = eo_now >= 0 ? p.ve[eo_now] : 0;
 
-  int step = 0, seg_index = 0;
+  int step = 0, seg_index = 0, stage = 0;
   while (step < nsteps) {
     // ---------------------------------------------------------- one segment
     const int b = cons.b, h = cons.seg / p.row_tiles;
@@ -316,27 +359,24 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     bool bad = false;
     const int rows = seq_rows(p, b, &bad);
     const int r_end = rows * p.G;
-    // this lane's two rows
-    int vis[2];
-    float f[2];
-    uint32_t a[kSteps][4];
+    // Queries as the 8-wide operand: this lane holds parts of rows 8 t + q8,
+    // and the statistics of rows 8 t + 2 c4 and 8 t + 2 c4 + 1.
+    int vis[kNT][2];
+    float f[kNT][2];
+    uint32_t qf[kNT][kSteps][2];
     int vis_min = len;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = rt * kDecRows + q8 + 8 * x;
-      const int i = r / p.G;
+    for (int t = 0; t < kNT; ++t) {
+      const int r = rt * C::kRows + 8 * t + q8;
       const bool on = r < r_end;
-      vis[x] = on ? row_sees(p, i, len, rows) : 0;
-      vis_min = min(vis_min, on ? vis[x] : len);
+      const int i = r / p.G;
       const __nv_bfloat16 *src =
-          p.q + (((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i) * D;
+          p.q + (((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i) * D + c4 * kChunks * 16;
       uint2 w[kSteps];
       uint32_t am = 0;
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
-        w[ks] = on ? *reinterpret_cast<const uint2 *>(src + (c4 + 4 * (ks >> 2)) * 16 +
-                                                      (ks & 3) * 4)
-                   : make_uint2(0, 0);
+        w[ks] = on ? *reinterpret_cast<const uint2 *>(src + 4 * ks) : make_uint2(0, 0);
         am = max_u16x2(am, w[ks].x & 0x7fff7fffu);
         am = max_u16x2(am, w[ks].y & 0x7fff7fffu);
       }
@@ -345,138 +385,165 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
       int ea = (int)(am >> 7) - 127;
       if (am < 0x80u || am >= 0x7f80u) ea = 0;  // no normal value, or not finite
-      ea = max(ea, -126 + 1);
-      const float sc = exp2i(-ea < -126 ? -126 : -ea);
-      const float back = exp2i(-ea < -126 ? 126 : ea);
-      f[x] = p.scale_log2 * back;
+      ea = min(ea, 126);
+      const float sc = exp2i(-ea);
+      const float fr = p.scale_log2 * exp2i(ea);
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
-        a[ks][x] = bf16x2_to_f16x2_scaled(w[ks].x, sc);
-        a[ks][2 + x] = bf16x2_to_f16x2_scaled(w[ks].y, sc);
+        qf[t][ks][0] = bf16x2_to_f16x2_scaled(w[ks].x, sc);
+        qf[t][ks][1] = bf16x2_to_f16x2_scaled(w[ks].y, sc);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int rx = rt * C::kRows + 8 * t + 2 * c4 + x;
+        vis[t][x] = rx < r_end ? row_sees(p, rx / p.G, len, rows) : 0;
+        vis_min = min(vis_min, rx < r_end ? vis[t][x] : len);
+        f[t][x] = __shfl_sync(0xffffffffu, fr, (2 * c4 + x) * 4);
       }
     }
     vis_min = __reduce_min_sync(0xffffffffu, vis_min);
 
-    float o[kTiles][4];
+    float o[kNT][kSteps][4];
+    float m[kNT][2], mo[kNT][2], l[kNT][2];
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
+      m[t][0] = m[t][1] = mo[t][0] = mo[t][1] = kDecNone;
+      l[t][0] = l[t][1] = 0.f;
+    }
 
     for (int n = 0; n < n_here; ++n, ++step) {
-      // issue the step kDecStages - 1 ahead, then wait for this one's copies
-      int ex_new = 1 << 16;
-      if (step + kDecStages - 1 < nsteps) {
-        ex_new = issue((step + kDecStages - 1) % kDecStages, next_id);
+      // issue the step kStages - 1 ahead, then wait for this one's copies
+      const bool none = eo_now < 0;
+      const int ke = ke_now, ve = ve_now;
+      eo_now = eo[1];
+      int eo_new = -1;
+      const int ahead = stage == 0 ? kStages - 1 : stage - 1;
+      if (step + kStages - 1 < nsteps) {
+        eo_new = issue(ahead, next_id);
         dec_advance(p, prod, segs);
-        next_id = step + kDecStages < nsteps ? fetch_page() : -2;
+        next_id = step + kStages < nsteps ? fetch_page() : -2;
       } else {
         cp_async_commit();
       }
-      cp_async_wait<kDecStages - 1>();
-      const int ex_now = ex[0];
 #pragma unroll
-      for (int s = 0; s + 1 < kDecStages - 1; ++s) ex[s] = ex[s + 1];
-      ex[kDecStages - 2] = ex_new;
+      for (int i = 0; i + 1 < kStages - 1; ++i) eo[i] = eo[i + 1];
+      eo[kStages - 2] = eo_new;
+      ke_now = eo_now >= 0 ? p.ke[eo_now] : 0;
+      ve_now = eo_now >= 0 ? p.ve[eo_now] : 0;
+      cp_async_wait<kStages - 1>();
+      __syncwarp();  // every lane's copies of this step
+      const uint8_t *st = smem + (warp * kStages + stage) * C::kStageBytes;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
       const int t0 = (cons.unit + n) * kDecUnit + warp * 16;
-      if (ex_now >> 16 || t0 >= len) continue;  // (warp-uniform)
-      const uint8_t *st = smem + (warp * kDecStages + step % kDecStages) * C::kStageBytes;
-      const float fk = exp2i((int)(int8_t)ex_now);
-      const int ev = (int8_t)(ex_now >> 8);
+      if (none) continue;  // no positions of this warp (warp-uniform)
+      const float fk = exp2i(ke);
+      const float ev = (float)ve;
 
-      // S = Q K^T of 16 positions
-      float s[2][4];
+      // S^T = K Q^T: 16 positions x 8 rows a tile; s[t][0, 1]: position q8,
+      // rows 2 c4 and 2 c4 + 1; s[t][2, 3]: position q8 + 8
+      float s[kNT][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      for (int t = 0; t < kNT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-          const uint4 w =
-              *reinterpret_cast<const uint4 *>(st + ((t * kChunks + j) * 32 + lane) * 16);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      for (int j = 0; j < kChunks; ++j) {
+        const uint4 w0 = *reinterpret_cast<const uint4 *>(st + (k_get ^ (16 * j)));
+        const uint4 w1 = *reinterpret_cast<const uint4 *>(st + (k_get ^ (16 * j)) + 8 * D);
+        const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ks = 4 * j + i;
-            mma_f16(s[t], a[ks][0], a[ks][1], a[ks][2], a[ks][3],
-                    e4m3x2_to_f16x2((uint16_t)(ww[i] & 0xffffu)),
-                    e4m3x2_to_f16x2((uint16_t)(ww[i] >> 16)));
-          }
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2x2(x0[i], a0, a2);
+          e4m3x4_to_f16x2x2(x1[i], a1, a3);
+#pragma unroll
+          for (int t = 0; t < kNT; ++t)
+            mma_f16(s[t], a0, a1, a2, a3, qf[t][4 * j + i][0], qf[t][4 * j + i][1]);
         }
       }
       const bool edge = t0 + 16 > vis_min;
-      float mx[2];
+      // z = s - m (log2 units), and how far m + ve lies above M: while no
+      // score passes m by more than 2^tau and no m + ve passes M, the
+      // references stay and nothing has to be reduced across the warp.
+      float z[kNT][4], over[kNT][2];
+      float top = -1.f;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float fx = f[x] * fk;
+      for (int t = 0; t < kNT; ++t)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float &y = s[t][2 * x + i];
-            y *= fx;
-            if (edge && t0 + t * 8 + 2 * c4 + i >= vis[x]) y = -INFINITY;
+        for (int x = 0; x < 2; ++x) {
+          const float fx = f[t][x] * fk;
+          z[t][x] = fmaf(s[t][x], fx, -m[t][x]);
+          z[t][2 + x] = fmaf(s[t][2 + x], fx, -m[t][x]);
+          if (edge) {
+            if (t0 + q8 >= vis[t][x]) z[t][x] = -INFINITY;
+            if (t0 + q8 + 8 >= vis[t][x]) z[t][2 + x] = -INFINITY;
           }
-        mx[x] = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
-      }
-      // references, and the factors that moving them takes
-      float up[2];
-      uint32_t pa[2][2];
-      bool moved = false;
+          over[t][x] = m[t][x] + ev - mo[t][x];
+          top = fmaxf(top, max3(z[t][x] - kDecTau, z[t][2 + x] - kDecTau, over[t][x]));
+        }
+      if (__any_sync(0xffffffffu, top > 0.f)) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float m_new = mx[x] > m[x] + kDecTau ? mx[x] : m[x];
-        const float co = mx[x] + (float)ev;
-        const float mo_new = co > mo[x] + kDecTau ? co : mo[x];
-        l[x] *= m_new == m[x] ? 1.f : ex2_approx(m[x] - m_new);
-        up[x] = mo_new == mo[x] ? 1.f : ex2_approx(mo[x] - mo_new);
-        moved |= mo_new != mo[x];
-        m[x] = m_new;
-        mo[x] = mo_new;
-        const float mu = m_new == -INFINITY ? 0.f : m_new;
-        // P = 2^(s - m), P' = P 2^(m + ve - M + 6)
-        const float lift =
-            ex2_approx(fminf((m_new == -INFINITY ? -200.f : m_new + (float)ev - mo_new) + kDecLift,
-                             120.f));
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float fx = f[t][x] * fk;
+            const bool see0 = z[t][x] != -INFINITY, see1 = z[t][2 + x] != -INFINITY;
+            const float y0 = s[t][x] * fx, y1 = s[t][2 + x] * fx;
+            float mx = fmaxf(see0 ? y0 : -INFINITY, see1 ? y1 : -INFINITY);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float m_new = mx > m[t][x] + kDecTau ? mx : m[t][x];
+            l[t][x] *= ex2_approx(m[t][x] - m_new);
+            m[t][x] = m_new;
+            if (see0) z[t][x] = fmaf(s[t][x], fx, -m_new);
+            if (see1) z[t][2 + x] = fmaf(s[t][2 + x], fx, -m_new);
+            const float mo_new = fmaxf(mo[t][x], m[t][x] + ev);
+            const float up = ex2_approx(mo[t][x] - mo_new);
+            mo[t][x] = mo_new;
+            over[t][x] = m[t][x] + ev - mo_new;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+              o[t][j][x] *= up;
+              o[t][j][2 + x] *= up;
+            }
+          }
+      }
+      uint32_t pb[kNT][2];
+#pragma unroll
+      for (int t = 0; t < kNT; ++t) {
         float pr[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float e = ex2_approx(s[t][2 * x + i] - mu);
-            l[x] += e;
-            pr[2 * t + i] = e * lift;
-          }
-        pa[0][x] = pack_f16x2(pr[0], pr[1]);
-        pa[1][x] = pack_f16x2(pr[2], pr[3]);
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          o[j][0] *= up[0];
-          o[j][1] *= up[0];
-          o[j][2] *= up[1];
-          o[j][3] *= up[1];
+        for (int x = 0; x < 2; ++x) {
+          // P = 2^(s - m), P' = P 2^(m + ve - M + lift)
+          const float lift = ex2_approx(over[t][x] + kDecLift);
+          const float e0 = ex2_approx(z[t][x]), e1 = ex2_approx(z[t][2 + x]);
+          l[t][x] += e0 + e1;
+          pr[x] = e0 * lift;
+          pr[2 + x] = e1 * lift;
         }
+        // as the 8-wide operand: positions 2 c4, 2 c4 + 1 (and + 8) of row q8
+        pb[t][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
+        pb[t][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
       }
-      // O += P' V
+      // O^T += V^T P'^T: lane q8's columns of tile j are kRun q8 + 2 j, + 1
       uint32_t w[4][kVw];
-      const uint8_t *sv = st + 16 * D;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {  // positions 2 c4, 2 c4 + 1, and these + 8
+        const uint8_t *sv = st + 16 * D + v_get[i & 1] + (i >> 1) * 8 * D;
         if constexpr (D == 128) {
-          const uint4 y = *reinterpret_cast<const uint4 *>(sv + (i * 32 + lane) * 16);
+          const uint4 y = *reinterpret_cast<const uint4 *>(sv);
           w[i][0] = y.x;
           w[i][1] = y.y;
           w[i][2] = y.z;
           w[i][3] = y.w;
         } else {
-          const uint2 y = *reinterpret_cast<const uint2 *>(sv + (i * 32 + lane) * 8);
+          const uint2 y = *reinterpret_cast<const uint2 *>(sv);
           w[i][0] = y.x;
           w[i][1] = y.y;
         }
       }
-      int i_lo = 0, i_hi = 0;  // rows in one go, or query by query
+      __syncwarp();  // this step's slot is read: the next copies may take it
       if (edge) {
         bool odd = false;
 #pragma unroll
@@ -489,12 +556,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           }
         }
         if (__any_sync(0xffffffffu, odd)) {
-          i_lo = rt * kDecRows / p.G;
-          i_hi = min(rows - 1, (rt * kDecRows + kDecRows - 1) / p.G);
+          // query by query, without the positions that one does not see
+          const int i_lo = rt * C::kRows / p.G;
+          const int i_hi = min(rows - 1, (rt * C::kRows + C::kRows - 1) / p.G);
           for (int i = i_lo; i <= i_hi; ++i) {
             const int see = row_sees(p, i, len, rows);
-            const int ra = rt * kDecRows + q8;
-            const bool on0 = ra / p.G == i, on1 = (ra + 8) / p.G == i;
             uint32_t z[4][kVw];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -502,131 +568,120 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               for (int y = 0; y < kVw; ++y)
                 z[k][y] = t0 + 2 * c4 + (k & 1) + (k >> 1) * 8 < see ? w[k][y] : 0u;
 #pragma unroll
-            for (int y = 0; y < kVw; ++y)
+            for (int t = 0; t < kNT; ++t) {
+              const int ra = rt * C::kRows + 8 * t + 2 * c4;
+              const bool on0 = ra / p.G == i, on1 = (ra + 1) / p.G == i;
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const uint32_t sel = half ? 0x7362 : 0x5140;
-                const uint32_t x0 = __byte_perm(z[0][y], z[1][y], sel);
-                const uint32_t x1 = __byte_perm(z[2][y], z[3][y], sel);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  float t[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma_f16(t, pa[0][0], pa[0][1], pa[1][0], pa[1][1],
-                          e4m3x2_to_f16x2((uint16_t)(x0 >> (16 * k))),
-                          e4m3x2_to_f16x2((uint16_t)(x1 >> (16 * k))));
-                  float(&oo)[4] = o[4 * y + 2 * half + k];
-                  if (on0) {
-                    oo[0] += t[0];
-                    oo[1] += t[1];
-                  }
-                  if (on1) {
-                    oo[2] += t[2];
-                    oo[3] += t[3];
-                  }
+              for (int j = 0; j < kSteps; ++j) {
+                const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x2x2(__byte_perm(z[0][j >> 1], z[1][j >> 1], sel), a0, a1);
+                e4m3x4_to_f16x2x2(__byte_perm(z[2][j >> 1], z[3][j >> 1], sel), a2, a3);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d, a0, a1, a2, a3, pb[t][0], pb[t][1]);
+                if (on0) {
+                  o[t][j][0] += d[0];
+                  o[t][j][2] += d[2];
+                }
+                if (on1) {
+                  o[t][j][1] += d[1];
+                  o[t][j][3] += d[3];
                 }
               }
+            }
           }
           continue;
         }
       }
 #pragma unroll
-      for (int y = 0; y < kVw; ++y)
+      for (int j = 0; j < kSteps; ++j) {
+        const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_f16x2x2(__byte_perm(w[0][j >> 1], w[1][j >> 1], sel), a0, a1);
+        e4m3x4_to_f16x2x2(__byte_perm(w[2][j >> 1], w[3][j >> 1], sel), a2, a3);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7362 : 0x5140;
-          const uint32_t x0 = __byte_perm(w[0][y], w[1][y], sel);
-          const uint32_t x1 = __byte_perm(w[2][y], w[3][y], sel);
-          mma_f16(o[4 * y + 2 * half], pa[0][0], pa[0][1], pa[1][0], pa[1][1],
-                  e4m3x2_to_f16x2((uint16_t)(x0 & 0xffffu)),
-                  e4m3x2_to_f16x2((uint16_t)(x1 & 0xffffu)));
-          mma_f16(o[4 * y + 2 * half + 1], pa[0][0], pa[0][1], pa[1][0], pa[1][1],
-                  e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)));
-        }
+        for (int t = 0; t < kNT; ++t) mma_f16(o[t][j], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+      }
     }
 
     // ---------------------------------------------------------- join the warps
     __syncthreads();  // the merge buffer is free
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      const int row = q8 + 8 * x;
-      if (c4 == 0) {
-        float *d = merge_s + (warp * kDecRows + row) * 4;
-        d[0] = m[x];
-        d[1] = mo[x];
-        d[2] = l[x];
-      }
+    for (int t = 0; t < kNT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float *d = merge_o + (warp * kDecRows + row) * C::kRowStride + (2 * c4 + i) * C::kRunStride;
+      for (int x = 0; x < 2; ++x) {
+        float ls = l[t][x];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 4);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 8);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+        const int row = 8 * t + 2 * c4 + x;
+        if (q8 == 0)
+          *reinterpret_cast<float4 *>(merge_s + (warp * C::kRows + row) * 4) =
+              make_float4(m[t][x], mo[t][x], ls, 0.f);
+        float *d = merge_o + (warp * C::kRows + row) * C::kRowStride + q8 * C::kRunStride;
 #pragma unroll
-        for (int j = 0; j < kTiles; j += 4)
-          *reinterpret_cast<float4 *>(d + j) =
-              make_float4(o[j][2 * x + i], o[j + 1][2 * x + i], o[j + 2][2 * x + i],
-                          o[j + 3][2 * x + i]);
+        for (int j = 0; j < kSteps; j += 2)
+          *reinterpret_cast<float4 *>(d + 2 * j) = make_float4(
+              o[t][j][x], o[t][j][2 + x], o[t][j + 1][x], o[t][j + 1][2 + x]);
       }
-    }
     __syncthreads();
     {
-      const int row = threadIdx.x >> 3, run = threadIdx.x & 7;
-      const int r = rt * kDecRows + row;
+      constexpr int kPer = kDecThreads / C::kRows;  // threads of a row
+      constexpr int kCols = D / kPer;               // columns of a thread
+      const int row = threadIdx.x / kPer, col = (threadIdx.x % kPer) * kCols;
+      const int r = rt * C::kRows + row;
       if (r < r_end) {
-        float mm = -INFINITY, mmo = -INFINITY, ll = 0.f;
-        float wt[kDecWarps];
+        float mm = kDecNone, mmo = kDecNone, ll = 0.f;
+        float4 st[kDecWarps];
 #pragma unroll
         for (int w2 = 0; w2 < kDecWarps; ++w2) {
-          const float *d = merge_s + (w2 * kDecRows + row) * 4;
-          mm = fmaxf(mm, d[0]);
-          mmo = fmaxf(mmo, d[1]);
+          st[w2] = *reinterpret_cast<const float4 *>(merge_s + (w2 * C::kRows + row) * 4);
+          mm = fmaxf(mm, st[w2].x);
+          mmo = fmaxf(mmo, st[w2].y);
         }
+        float out[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) out[j] = 0.f;
+        const float *d0 = merge_o + row * C::kRowStride + (col / C::kRun) * C::kRunStride +
+                          col % C::kRun;
 #pragma unroll
         for (int w2 = 0; w2 < kDecWarps; ++w2) {
-          const float *d = merge_s + (w2 * kDecRows + row) * 4;
           // nothing seen: l is 0 (a NaN score leaves l NaN, which has to stay)
-          ll += d[2] == 0.f ? 0.f : d[2] * ex2_approx(d[0] - mm);
-          wt[w2] = d[2] == 0.f ? 0.f : ex2_approx(d[1] - mmo);
-        }
-        float out[C::kRun];
+          const bool none = st[w2].z == 0.f;
+          ll += none ? 0.f : st[w2].z * ex2_approx(st[w2].x - mm);
+          const float wt = none ? 0.f : ex2_approx(st[w2].y - mmo);
+          const float *d = d0 + w2 * C::kRows * C::kRowStride;
 #pragma unroll
-        for (int j = 0; j < C::kRun; ++j) out[j] = 0.f;
-#pragma unroll
-        for (int w2 = 0; w2 < kDecWarps; ++w2) {
-          const float *d = merge_o + (w2 * kDecRows + row) * C::kRowStride + run * C::kRunStride;
-#pragma unroll
-          for (int j = 0; j < C::kRun; j += 4) {
+          for (int j = 0; j < kCols; j += 4) {
             const float4 y = *reinterpret_cast<const float4 *>(d + j);
-            out[j] = fmaf(wt[w2], y.x, out[j]);
-            out[j + 1] = fmaf(wt[w2], y.y, out[j + 1]);
-            out[j + 2] = fmaf(wt[w2], y.z, out[j + 2]);
-            out[j + 3] = fmaf(wt[w2], y.w, out[j + 3]);
+            out[j] = fmaf(wt, y.x, out[j]);
+            out[j + 1] = fmaf(wt, y.y, out[j + 1]);
+            out[j + 2] = fmaf(wt, y.z, out[j + 2]);
+            out[j + 3] = fmaf(wt, y.w, out[j + 3]);
           }
         }
         if (whole) {
           const int i = r / p.G;
           const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
-          // 2^(M - 6 - m) / l, in two factors (M - m is a value exponent)
+          // 2^(M - lift - m) / l, in two factors (M - m is a value exponent)
           const float half = ll == 0.f ? 0.f : ex2_approx(0.5f * (mmo - kDecLift - mm));
           const float inv = ll == 0.f ? 0.f : half / ll;
-          uint32_t pk[C::kRun / 2];
+          uint2 *dst = reinterpret_cast<uint2 *>(p.o + orow * D + col);
 #pragma unroll
-          for (int j = 0; j < C::kRun / 2; ++j)
-            pk[j] = pack_bf16x2(out[2 * j] * inv * half, out[2 * j + 1] * inv * half);
-          uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + run * C::kRun);
-#pragma unroll
-          for (int j = 0; j < C::kRun / 8; ++j)
-            dst[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-          if (run == 0)
+          for (int j = 0; j < kCols; j += 4)
+            dst[j / 4] = make_uint2(pack_bf16x2(out[j] * inv * half, out[j + 1] * inv * half),
+                                    pack_bf16x2(out[j + 2] * inv * half, out[j + 3] * inv * half));
+          if (col == 0)
             p.lse[orow] =
                 ll == 0.f ? -INFINITY : (mm + lg2_approx(ll)) * 0.69314718055994531f;
         } else {
-          float *d = p.part + (((size_t)blockIdx.x * 2 + (seg_index > 0)) * kDecRows + row) *
+          float *d = p.part + (((size_t)blockIdx.x * 2 + (seg_index > 0)) * C::kRows + row) *
                                   (D + 4);
 #pragma unroll
-          for (int j = 0; j < C::kRun; j += 4)
-            *reinterpret_cast<float4 *>(d + run * C::kRun + j) =
+          for (int j = 0; j < kCols; j += 4)
+            *reinterpret_cast<float4 *>(d + col + j) =
                 make_float4(out[j], out[j + 1], out[j + 2], out[j + 3]);
-          if (run == 0) *reinterpret_cast<float4 *>(d + D) = make_float4(mm, mmo, ll, 0.f);
+          if (col == 0) *reinterpret_cast<float4 *>(d + D) = make_float4(mm, mmo, ll, 0.f);
         }
       }
     }
@@ -650,26 +705,29 @@ __global__ void __launch_bounds__(D)
   const int h = seg / p.row_tiles, rt = seg - h * p.row_tiles;
   bool bad = false;
   const int rows = seq_rows(p, b, &bad);
-  const int r = rt * kDecRows + row;
-  if (r >= rows * p.G) return;
+  const int r = rt * p.tile_rows + row;
   kv8_scan(p, kDecUnit, segs, 0, b, &place, red);
   const int units = seq_units(p, b, kDecUnit);
   const long long share = max(1LL, (place.total + p.ctas - 1) / p.ctas);
   const long long s0 = place.prefix + (long long)seg * units;
-  const int c0 = (int)(s0 / share), c1 = (int)((s0 + units - 1) / share);
-  if (c0 == c1) return;
+  const int c0 = (int)(s0 / share), c1 = (int)((s0 + max(units, 1) - 1) / share);
+  // All above reads only what the launch before leaves alone.  Every block
+  // waits, so that this launch's end means the end of the one before too.
+  grid_wait();
+  if (r >= rows * p.G || c0 == c1) return;
   // run c0's partial is its first segment's only if it starts where the segment does
   const float *base = p.part + (size_t)row * (D + 4);
-  const size_t slot = (size_t)kDecRows * (D + 4);
+  const size_t slot = (size_t)p.tile_rows * (D + 4);
   const int first0 = c0 * share == s0 ? 0 : 1;
   auto at = [&](int c) { return base + ((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot; };
-  float mm = -INFINITY, mmo = -INFINITY;
+  float mm = kDecNone, mmo = kDecNone;
+#pragma unroll 8
   for (int c = c0; c <= c1; ++c) {
     mm = fmaxf(mm, at(c)[D]);
     mmo = fmaxf(mmo, at(c)[D + 1]);
   }
   float ll = 0.f, out = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int c = c0; c <= c1; ++c) {
     const float *d = at(c);
     const float l = d[D + 2];
