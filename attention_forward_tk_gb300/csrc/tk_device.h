@@ -2,6 +2,8 @@
 // device: set up once per device (tk_attn.cu), read by every entry point.
 #pragma once
 
+#include <cuda.h>
+
 #include <cstddef>
 #include <cstdint>
 
@@ -18,6 +20,11 @@ struct DeviceView {
 // The current device, set up on first use.  Returns TK_ATTN_OK or the status
 // the calling entry point has to return.
 int device_view(DeviceView *out);
+
+// Tensor map of a byte matrix [rows, row_bytes] (row_bytes 64 or 128): boxes of
+// box_rows whole rows, swizzled over the row's length.
+bool make_map_bytes(CUtensorMap *map, const void *ptr, long long rows, int row_bytes,
+                    int box_rows);
 
 // [a, a + na) and [b, b + nb) share a byte.
 inline bool ranges_overlap(uintptr_t a, size_t na, uintptr_t b, size_t nb) {

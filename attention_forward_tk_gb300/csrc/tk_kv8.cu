@@ -1,6 +1,7 @@
 // tk_kv8.cu -- host side of the 8-bit paged cache: argument checks and
 // launches of the write, the read-back and the attention over it (the C ABI is
-// in tk_attn.h; the kernels in tk_kv8_copy.cuh and tk_kv8_decode.cuh).
+// in tk_attn.h; the kernels in tk_kv8_copy.cuh, tk_kv8_decode.cuh and
+// tk_kv8_chunk.cuh).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -10,6 +11,7 @@
 #include "tk_attn.h"
 #include "tk_device.h"
 #include "tk_kv8.h"
+#include "tk_kv8_chunk.cuh"
 #include "tk_kv8_copy.cuh"
 #include "tk_kv8_decode.cuh"
 
@@ -30,13 +32,23 @@ bool configure_decode() {
                               DecCfg<D, kNT>::kSmem) == cudaSuccess;
 }
 
+template <int D>
+bool configure_chunk() {
+  if (cudaFuncSetAttribute(tk_kv8_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           ChunkCfg<D>::kSmemAlloc) != cudaSuccess)
+    return false;
+  // the register split between warpgroups assumes exactly 128 a thread at launch
+  cudaFuncAttributes fa;
+  return cudaFuncGetAttributes(&fa, tk_kv8_chunk_kernel<D>) == cudaSuccess && fa.numRegs == 128;
+}
+
 int kv8_device(DeviceView *dv) {
   const int st = device_view(dv);
   if (st) return st;
   Kv8Device &d = g_kv8_dev[dv->index];
   std::call_once(d.once, [&d] {
     d.ok = configure_decode<64, 1>() && configure_decode<64, 2>() && configure_decode<128, 1>() &&
-           configure_decode<128, 2>();
+           configure_decode<128, 2>() && configure_chunk<64>() && configure_chunk<128>();
   });
   return d.ok ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }
@@ -52,7 +64,7 @@ int check_geom(const void *k_cache, const void *v_cache, const void *k_exp, cons
   if (((uintptr_t)k_cache | (uintptr_t)v_cache) & 15u || (uintptr_t)table & 3u)
     return TK_ATTN_ERR_UNSUPPORTED;
   if ((long long)max_pages * page > 0x7fffffffLL || 2LL * Hkv > 65535 ||
-      (long long)num_pages * Hkv > 0x7fffffffLL)
+      (long long)num_pages * Hkv * page > 0x7fffffffLL)
     return TK_ATTN_ERR_UNSUPPORTED;
   return TK_ATTN_OK;
 }
@@ -223,43 +235,65 @@ extern "C" int tk_attn_kv8_read(const void *k_cache, const void *v_cache, const 
 namespace tkattn {
 namespace {
 
-// Query rows of a tile: eight where the call has no more, else sixteen.
+// At most 16 query rows a (sequence, key/value head) stream the cache past
+// 8-row or 16-row tiles; more go to the 128-row tiles of the tensor core.
+bool few_rows(int G, int Nq) { return (long long)Nq * G <= 16; }
 int tile_rows(int G, int Nq) { return (long long)Nq * G <= 8 ? 8 : 16; }
-int row_tiles(int G, int Nq) {
-  const int t = tile_rows(G, Nq);
-  return (int)(((long long)Nq * G + t - 1) / t);
-}
 // Runs the work is cut into: the CTAs that fit on the device at once.
-int decode_ctas(const DeviceView &dv, int rows) {
-  return (rows == 8 ? DecCfg<128, 1>::kCtasPerSm : DecCfg<128, 2>::kCtasPerSm) * dv.num_sms;
+int run_count(const DeviceView &dv, int G, int Nq) {
+  if (!few_rows(G, Nq)) return dv.num_sms;
+  return (tile_rows(G, Nq) == 8 ? DecCfg<128, 1>::kCtasPerSm : DecCfg<128, 2>::kCtasPerSm) *
+         dv.num_sms;
 }
 
 bool sizes_ok(int B, int H, int Hkv, int Nq, int D) {
   return B > 0 && H > 0 && Hkv > 0 && Nq > 0 && H % Hkv == 0 && (D == 64 || D == 128);
 }
 
-size_t workspace_for(const DeviceView &dv, int G, int Nq, int D) {
-  const int t = tile_rows(G, Nq);
-  return (size_t)decode_ctas(dv, t) * 2 * t * (D + 4) * sizeof(float);
+size_t prefix_bytes(int B) { return ((size_t)B * 8 + 8 + 15) / 16 * 16; }
+
+size_t workspace_for(const DeviceView &dv, int B, int G, int Nq, int D) {
+  const int t = few_rows(G, Nq) ? tile_rows(G, Nq) : kChunkRows;
+  return prefix_bytes(B) + (size_t)run_count(dv, G, Nq) * 2 * t * (D + 4) * sizeof(float);
 }
 
-template <int D, int kNT>
-cudaError_t launch_decode(const Kv8AttnParams &p, dim3 merge_grid, cudaStream_t s) {
-  tk_kv8_decode_kernel<D, kNT><<<p.ctas, kDecThreads, DecCfg<D, kNT>::kSmem, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // The merge starts while the runs still work, finds what it has to do, and
-  // waits for them on the device.
+// A merge that starts while the launch before still works, finds what it has
+// to do, and waits for it on the device.
+template <typename Kernel>
+cudaError_t launch_merge(Kernel kernel, dim3 grid, int threads, const Kv8AttnParams &p,
+                         cudaStream_t s) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = merge_grid;
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tk_kv8_merge_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D, int kNT>
+cudaError_t launch_decode(const Kv8AttnParams &p, cudaStream_t s) {
+  tk_kv8_decode_kernel<D, kNT><<<p.ctas, kDecThreads, DecCfg<D, kNT>::kSmem, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_merge(tk_kv8_merge_kernel<D>, dim3(p.g.Hkv, p.B, p.Nq * p.G), D, p,
+                      s);
+}
+
+template <int D>
+cudaError_t launch_chunk(const Kv8AttnParams &p, cudaStream_t s) {
+  const long long rows = (long long)p.g.num_pages * p.g.Hkv * p.g.page;
+  CUtensorMap tk, tv;
+  if (!make_map_bytes(&tk, p.k, rows, D, p.g.page) || !make_map_bytes(&tv, p.v, rows, D, p.g.page))
+    return cudaErrorInvalidValue;
+  tk_kv8_chunk_kernel<D><<<p.ctas, kChunkThreads, ChunkCfg<D>::kSmemAlloc, s>>>(tk, tv, p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_merge(tk_kv8_chunk_merge_kernel<D>,
+                      dim3((unsigned)(((long long)p.Nq * p.G + 7) / 8), p.g.Hkv, p.B), 256, p, s);
 }
 
 }  // namespace
@@ -268,7 +302,7 @@ cudaError_t launch_decode(const Kv8AttnParams &p, dim3 merge_grid, cudaStream_t 
 extern "C" size_t tk_attn_fwd_kv8_workspace_bytes(int B, int H, int Hkv, int Nq, int D) {
   DeviceView dv;
   if (!sizes_ok(B, H, Hkv, Nq, D) || device_view(&dv)) return 0;
-  return workspace_for(dv, H / Hkv, Nq, D);
+  return workspace_for(dv, B, H / Hkv, Nq, D);
 }
 
 extern "C" int tk_attn_fwd_kv8_check_args(const void *q, const void *k_cache, const void *v_cache,
@@ -320,7 +354,7 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
   if (st) return st;
   DeviceView dv;
   if ((st = kv8_device(&dv))) return st;
-  if (workspace_bytes < workspace_for(dv, H / Hkv, Nq, D)) return TK_ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < workspace_for(dv, B, H / Hkv, Nq, D)) return TK_ATTN_ERR_INVALID_ARG;
   Kv8AttnParams p;
   p.g = geom(num_pages, Hkv, page, D, max_pages, table_stride);
   p.page_log2 = log2i(page);
@@ -341,17 +375,17 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
   p.causal = causal != 0;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.tile_rows = tile_rows(p.G, Nq);
-  p.row_tiles = row_tiles(p.G, Nq);
-  p.ctas = decode_ctas(dv, p.tile_rows);
+  p.ctas = run_count(dv, p.G, Nq);
   p.err = dv.err_word;
-  p.part = static_cast<float *>(workspace);
+  p.prefix = static_cast<long long *>(workspace);
+  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + prefix_bytes(B));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const long long rows = (long long)Nq * p.G;
-  const dim3 merge_grid(Hkv * p.row_tiles, B, rows < p.tile_rows ? (int)rows : p.tile_rows);
-  const bool one = p.tile_rows == 8;
-  const cudaError_t e = D == 64 ? (one ? launch_decode<64, 1>(p, merge_grid, s)
-                                       : launch_decode<64, 2>(p, merge_grid, s))
-                                : (one ? launch_decode<128, 1>(p, merge_grid, s)
-                                       : launch_decode<128, 2>(p, merge_grid, s));
+  cudaError_t e;
+  if (!few_rows(p.G, Nq))
+    e = D == 64 ? launch_chunk<64>(p, s) : launch_chunk<128>(p, s);
+  else if (p.tile_rows == 8)
+    e = D == 64 ? launch_decode<64, 1>(p, s) : launch_decode<128, 1>(p, s);
+  else
+    e = D == 64 ? launch_decode<64, 2>(p, s) : launch_decode<128, 2>(p, s);
   return e == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }

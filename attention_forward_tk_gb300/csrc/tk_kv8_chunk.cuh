@@ -1,0 +1,1015 @@
+// tk_kv8_chunk.cuh -- attention of many query rows over the 8-bit paged cache
+// (prefill chunks, many drafted tokens, wide head groups) on the tensor cores.
+//
+// The operation is tk_kv8_decode.cuh's; here a (sequence, key/value head) has
+// more query rows than that kernel's tiles.  Rows r = i * G + g are cut into
+// units of 256 (two tiles of 128); a unit visits the 128-position key tiles
+// its rows see.  The list of (unit, key tile) steps is cut into equal runs, one
+// for each CTA (the lengths live on the device, every CTA finds its run); a unit
+// that several runs share leaves partial results that a second kernel merges.
+//
+// Products:
+//   S = Q K^T   kind::f8f6f4: the key codes go to the tensor core as they lie
+//               in the cache.  A query row is scaled by a power of two to a
+//               largest magnitude in [128, 256) and split in two E4M3 terms,
+//               hi = rn(q), lo = rn(q - hi): bf16's eight bits are two times
+//               E4M3's four, so the split is exact but for elements below 2^-9
+//               of the row's largest (off by at most 2^-17 of it).  Two fp8
+//               products take the time of one in bf16 and no conversion.
+//               Each page's 2^ke multiplies its scores in fp32.
+//   O = P V     kind::f16: P in fp16 (four times bf16's precision), the value
+//               codes converted to fp16 in shared memory and multiplied by
+//               2^(ve - E + 6), E the largest value exponent of the run so far
+//               (exact while a page's lies within 2^21 of it); when E grows, O
+//               is rescaled.
+// The softmax is tk_attn_fwd.cuh's: one thread a row, a lazily moved maximum,
+// the fp32 sum of the unrounded P, the rounding of each tile's largest P
+// carried into the divisor.
+//
+// Roles (one CTA an SM, 512 threads):
+//   warps 0-3, 4-7  softmax of tile 0, 1; at a unit's start they convert their
+//                   tile's queries (their last scores being in hand, no product
+//                   still reads them)
+//   warps 8-11      value conversion, and the epilogue
+//   warp 12         tensor-core issue; warp 14: TMA, a lane a page
+// A NaN value code would spread over a tile's rows through 0 * NaN: codes are
+// replaced by 0 and the first position of each column that held one is kept;
+// rows that see that position get NaN in that column.
+//
+// Every wait is bounded as in tk_attn_fwd.cuh.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "sm103_ptx.cuh"
+#include "tk_device.h"
+#include "tk_kv8.h"
+#include "tk_kv8_copy.cuh"
+#include "tk_kv8_decode.cuh"
+
+namespace tkattn {
+
+constexpr int kChunkThreads = 512;
+constexpr int kChunkRows = 256;   // query rows of a unit
+constexpr float kChunkTau = 8.f;  // lazy maximum: P <= 2^8
+constexpr int kChunkLift = 6;     // value codes are lifted by 2^6
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int kRaw = 128 * D;                   // a tile of codes
+  static constexpr int kQTile = D == 128 ? 32768 : 16384;  // hi and lo of 128 rows
+  static constexpr int kKs = D == 128 ? 3 : 4;           // key ring
+  static constexpr int kVs = D == 128 ? 2 : 4;           // value ring
+  static constexpr int kV16 = 128 * D * 2;               // a converted value tile
+  static constexpr int kV16s = 2;
+  static constexpr int kOffK = 2 * kQTile;
+  static constexpr int kOffV = kOffK + kKs * kRaw;
+  static constexpr int kOffV16 = kOffV + kVs * kRaw;
+  static constexpr int kSmem = kOffV16 + kV16s * kV16;
+  static constexpr int kSmemAlloc = kSmem + 1024;  // + alignment slack
+  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+};
+
+struct ChunkShared {
+  uint64_t q_full[2];     // tile's queries converted        (4 softmax warps)
+  uint64_t k_full[4];     // key tile landed                 (1 + tx)
+  uint64_t k_empty[4];    // both tiles' S done with it      (commit)
+  uint64_t v_full[4];     // value tile landed               (1 + tx)
+  uint64_t v_empty[4];    // converted                       (4 converter warps)
+  uint64_t v_ready[2];    // fp16 values ready               (4 converter warps)
+  uint64_t v_free[2];     // both tiles' P V done with them  (commit)
+  uint64_t s_full[2];     // S of tile t complete            (commit)
+  uint64_t p_full[2];     // P of tile t written             (4 softmax warps)
+  uint64_t fin_full[2][2];  // [parity][tile] final m, l     (4 softmax warps)
+  uint64_t o_full[2];     // tile's last P V of a unit done  (commit)
+  uint64_t o_free[2];     // epilogue has read O             (4 converter warps)
+  uint64_t conv_bar;      // converter warps, once a unit    (4 converter warps)
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+  // run
+  Kv8Place place;
+  long long red[kChunkThreads / 32];
+  int start_h, start_mb, start_j;
+  // per step, eight deep: a slot is rewritten only when every reader is four steps on
+  alignas(16) float k_scale[8][8];  // 2^ke of the tile's eight runs of 16 positions
+  int k_valid[8];         // bit g: run g lies in a page that could be read
+  int v_exp8[8][8];       // value exponents of the runs
+  int v_exp[2];           // exponent the converted tile carries (6 - E)
+  float m_fin[2][2][128], l_fin[2][2][128], lc_fin[2][2][128];  // [parity][tile][row]
+  // eight segments deep: a converter warp is at most two tiles ahead of another
+  int nan_any[8];
+  int nan_pos[8][128];    // [segment][column]: first position that held a NaN
+};
+
+__device__ __forceinline__ void chunk_abort(ChunkShared &sb, int *err) {
+  sb.abort = 1;
+  atomicCAS(err, 0, kDevErrTimeout);
+}
+
+// Key tiles that rows [first, first + 128) of a sequence with `rows` queries
+// and length len visit (0: no such row).
+__device__ __forceinline__ int chunk_tiles(const Kv8AttnParams &p, int first, int len, int rows) {
+  const int r_end = rows * p.G;
+  if (first >= r_end) return 0;
+  const int i = min(first + 127, r_end - 1) / p.G;
+  return max(1, (row_sees(p, i, len, rows) + 127) / 128);
+}
+
+struct ChunkSeq {
+  int len, rows, units;  // units: 256-row units of a head
+};
+__device__ __forceinline__ ChunkSeq chunk_seq(const Kv8AttnParams &p, int b) {
+  bool bad = false;
+  ChunkSeq s;
+  s.len = seq_len(p, b, &bad);
+  s.rows = seq_rows(p, b, &bad);
+  s.units = (s.rows * p.G + kChunkRows - 1) / kChunkRows;
+  return s;
+}
+__device__ __forceinline__ int chunk_cost(const Kv8AttnParams &p, const ChunkSeq &s, int mb) {
+  return max(chunk_tiles(p, mb * kChunkRows, s.len, s.rows),
+             chunk_tiles(p, mb * kChunkRows + 128, s.len, s.rows));
+}
+__device__ __forceinline__ long long chunk_seq_cost(const Kv8AttnParams &p, int b) {
+  const ChunkSeq s = chunk_seq(p, b);
+  long long c = 0;
+  for (int mb = 0; mb < s.units; ++mb) c += chunk_cost(p, s, mb);
+  return c;
+}
+
+// The CTA's run of steps, one segment (part of a unit) after another.
+struct ChunkRun {
+  int b, h, mb, j;  // next segment's unit and key tile
+  long long left;   // steps left in the run
+  ChunkSeq seq;
+  // the current segment
+  int sb, sh, smb, j0, n0, n1, n;
+  ChunkSeq sseq;
+  bool whole;
+
+  __device__ __forceinline__ bool next(const Kv8AttnParams &p) {
+    if (left == 0) return false;
+    const int t0 = chunk_tiles(p, mb * kChunkRows, seq.len, seq.rows);
+    const int t1 = chunk_tiles(p, mb * kChunkRows + 128, seq.len, seq.rows);
+    const int cost = max(t0, t1);
+    sb = b;
+    sh = h;
+    smb = mb;
+    sseq = seq;
+    j0 = j;
+    n = (int)min((long long)(cost - j), left);
+    n0 = min(max(t0 - j, 0), n);
+    n1 = min(max(t1 - j, 0), n);
+    whole = j == 0 && n == cost;
+    left -= n;
+    j += n;
+    if (j == cost) {
+      j = 0;
+      if (++mb == seq.units) {
+        mb = 0;
+        if (++h == p.g.Hkv) {
+          h = 0;
+          while (++b < p.B) {
+            seq = chunk_seq(p, b);
+            if (seq.units > 0) break;
+          }
+        }
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands, fp32 accumulation.
+template <uint32_t kAcc>
+__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                           uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(kAcc)
+      : "memory");
+}
+
+// kind::f8f6f4, E4M3 x E4M3 -> fp32, both operands K-major (format codes 0).
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// High word of a descriptor with the 64-byte swizzle.
+__host__ __device__ constexpr uint32_t sdesc_sw64_hi(uint32_t sbo) {
+  return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (4u << 29);
+}
+
+// Convert one tile's query rows: warp w of the tile takes rows [32 w, 32 w + 32).
+// Returns this lane's row's score factor scale_log2 * 2^(its exponent).
+template <int D>
+__device__ __forceinline__ float chunk_queries(const Kv8AttnParams &p, int b, int h, int first,
+                                               int r_end, int w, int lane, uint8_t *tile) {
+  constexpr int kLanes = D / 8;           // lanes of a row, 8 values each
+  constexpr int kPerIt = 32 / kLanes;     // rows a pass
+  constexpr int kIts = 32 / kPerIt;
+  const int l = lane % kLanes, sub = lane / kLanes;
+  float mine = 1.f;
+#pragma unroll 1
+  for (int it0 = 0; it0 < kIts; it0 += 4) {
+    if (first + w * 32 + it0 * kPerIt >= r_end) break;  // no row left (warp-uniform)
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = first + w * 32 + (it0 + u) * kPerIt + sub;
+      const int i = r / p.G;
+      v[u] = r < r_end ? *reinterpret_cast<const uint4 *>(
+                             p.q + (((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i) * D +
+                             l * 8)
+                       : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = w * 32 + (it0 + u) * kPerIt + sub;  // row of the tile
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t am = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) am = max_u16x2(am, x[i] & 0x7fff7fffu);
+      am = max(am & 0xffffu, am >> 16);
+#pragma unroll
+      for (int d = kLanes / 2; d > 0; d >>= 1)
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, d));
+      int ea = (int)(am >> 7) - 127;
+      if (am < 0x80u) ea = 7;  // no normal value
+      ea = max(ea, -119);
+      const bool odd = am >= 0x7f80u;  // a NaN or an infinity: the row's scores are NaN
+      const float sc = odd ? 0.f : exp2i(7 - ea);
+      const float fr = odd ? __uint_as_float(0x7fc00000u) : p.scale_log2 * exp2i(ea - 7);
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t hc = 0, lc = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t y = x[2 * i + k];
+          const float a = __uint_as_float(y << 16) * sc, c = __uint_as_float(y & 0xffff0000u) * sc;
+          const uint32_t code = pack_e4m3x2(a, c);
+          const float2 back = e4m3x2_to_float2((uint16_t)code);
+          hc |= code << (16 * k);
+          lc |= pack_e4m3x2(a - back.x, c - back.y) << (16 * k);
+        }
+        hi[i] = hc;
+        lo[i] = lc;
+      }
+      const int piece = l >> 1, half = (l & 1) * 8;
+      uint8_t *line = tile + row * 128;
+      *reinterpret_cast<uint2 *>(line + ((piece ^ (row & 7)) << 4) + half) =
+          make_uint2(hi[0], hi[1]);
+      if constexpr (D == 128)
+        *reinterpret_cast<uint2 *>(line + 16384 + ((piece ^ (row & 7)) << 4) + half) =
+            make_uint2(lo[0], lo[1]);
+      else
+        *reinterpret_cast<uint2 *>(line + (((4 + piece) ^ (row & 7)) << 4) + half) =
+            make_uint2(lo[0], lo[1]);
+      // lane kPerIt * (it0 + u) + s owns row s of this pass
+      const float theirs = __shfl_sync(0xffffffffu, fr, (lane % kPerIt) * kLanes);
+      if (lane / kPerIt == it0 + u) mine = theirs;
+    }
+  }
+  return mine;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    tk_kv8_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ Kv8AttnParams p) {
+  using C = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ChunkShared sb;
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile int *abort_flag = &sb.abort;
+  const Kv8Geom &g = p.g;
+
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sb.q_full[t], 4);
+      mbar_init(&sb.v_ready[t], 4);
+      mbar_init(&sb.v_free[t], 1);
+      mbar_init(&sb.s_full[t], 1);
+      mbar_init(&sb.p_full[t], 4);
+      mbar_init(&sb.fin_full[0][t], 4);
+      mbar_init(&sb.fin_full[1][t], 4);
+      mbar_init(&sb.o_full[t], 1);
+      mbar_init(&sb.o_free[t], 4);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sb.k_full[s], 1);
+      mbar_init(&sb.k_empty[s], 1);
+      mbar_init(&sb.v_full[s], 1);
+      mbar_init(&sb.v_empty[s], 4);
+    }
+    mbar_init(&sb.conv_bar, 4);
+    mbar_init(&sb.mma_done, 1);
+    sb.abort = 0;
+    for (int i = 0; i < 8; ++i) sb.nan_any[i] = 0;
+    fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < 8 * 128; i += kChunkThreads)
+    sb.nan_pos[i >> 7][i & 127] = 0x7fffffff;
+  if (warp == 12) {
+    tmem_alloc(&sb.tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == 14 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (blockIdx.x == 0) {  // report what is out of range, once
+    bool bad = false;
+    for (int b = threadIdx.x; b < p.B; b += kChunkThreads) {
+      seq_len(p, b, &bad);
+      seq_rows(p, b, &bad);
+    }
+    if (bad) atomicCAS(p.err, 0, kDevErrIndex);
+  }
+  kv8_scan(
+      p, [&](int b) { return chunk_seq_cost(p, b) * p.g.Hkv; }, blockIdx.x, -1, &sb.place, sb.red,
+      blockIdx.x == 0 ? p.prefix : nullptr);
+  const long long share = max(1LL, (sb.place.total + p.ctas - 1) / p.ctas);
+  const long long u0 = blockIdx.x * share;
+  const long long steps = min(share, sb.place.total - u0);
+  if (threadIdx.x == 0 && steps > 0) {
+    const long long l = u0 - sb.place.prefix;
+    const ChunkSeq s = chunk_seq(p, sb.place.b);
+    const long long per_head = chunk_seq_cost(p, sb.place.b);
+    sb.start_h = (int)(l / per_head);
+    long long r = l - sb.start_h * per_head;
+    int mb = 0;
+    while (true) {
+      const int c = chunk_cost(p, s, mb);
+      if (r < c) break;
+      r -= c;
+      ++mb;
+    }
+    sb.start_mb = mb;
+    sb.start_j = (int)r;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sb.tmem_base;
+  ChunkRun run;
+  run.left = max(0LL, steps);
+  if (steps > 0) {
+    run.b = sb.place.b;
+    run.h = sb.start_h;
+    run.mb = sb.start_mb;
+    run.j = sb.start_j;
+    run.seq = chunk_seq(p, run.b);
+  }
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::: "memory");
+    const int t = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;  // row in tile == TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + (t ? C::kColS1 : C::kColS0);
+    const uint32_t tO = tmem + lane_off + (t ? C::kColO1 : C::kColO0);
+    uint32_t s_phase = 0;
+    uint32_t step0 = 0;  // steps of the run before this segment
+    uint32_t part = 0;   // segments this tile took part in
+    while (run.next(p)) {
+      const int n_t = t ? run.n1 : run.n0;
+      if (n_t == 0) {
+        step0 += run.n;
+        continue;
+      }
+      const int first = run.smb * kChunkRows + t * 128;
+      const int r_end = run.sseq.rows * p.G;
+      const float c =
+          chunk_queries<D>(p, run.sb, run.sh, first, r_end, warp & 3, lane, smem + t * C::kQTile);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.q_full[t]);
+      const int r = first + row;
+      const int vis = r < r_end ? row_sees(p, r / p.G, run.sseq.len, run.sseq.rows) : 0;
+      // Warps whose 32 rows all lie past the last one keep the protocol only.
+      const bool idle = first + (warp & 3) * 32 >= r_end;
+      const int vis_min = __reduce_min_sync(0xffffffffu, r < r_end ? vis : 0x7fffffff);
+      float m_run = -INFINITY, l_run = 0.f, lc_run = 0.f;
+      int e_cur = 0;
+      for (int j = 0; j < n_t; ++j) {
+        if (!mbar_wait(&sb.s_full[t], s_phase, abort_flag)) {
+          chunk_abort(sb, p.err);
+          goto done;
+        }
+        s_phase ^= 1;
+        const uint32_t idx = step0 + j;
+        if (idle) {
+          if (!mbar_wait(&sb.v_ready[idx % C::kV16s], (idx / C::kV16s) & 1, abort_flag)) {
+            chunk_abort(sb, p.err);
+            goto done;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sb.p_full[t]);
+            if (j == n_t - 1) mbar_arrive(&sb.fin_full[part & 1][t]);
+          }
+          continue;
+        }
+        tc_fence_after_sync();
+        uint32_t s[128];
+        tmem_ld_32x32b_x32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+        tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+        tmem_ld_32x32b_x32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+        tmem_ld_32x32b_x32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+        // each run of 16 positions has its page's factor
+        float cg[8];
+        {
+          const float4 a = *reinterpret_cast<const float4 *>(&sb.k_scale[idx & 7][0]);
+          const float4 d = *reinterpret_cast<const float4 *>(&sb.k_scale[idx & 7][4]);
+          cg[0] = a.x * c;
+          cg[1] = a.y * c;
+          cg[2] = a.z * c;
+          cg[3] = a.w * c;
+          cg[4] = d.x * c;
+          cg[5] = d.y * c;
+          cg[6] = d.z * c;
+          cg[7] = d.w * c;
+        }
+        const int valid = sb.k_valid[idx & 7];
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 128; ++i) reg_barrier(s[i]);
+        const int k0 = (run.j0 + j) * 128;
+        if (k0 + 128 > vis_min || valid != 0xff) {
+          const int lim = vis - k0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= lim || !(valid >> (i >> 4) & 1)) s[i] = __float_as_uint(-INFINITY);
+        }
+        float m_cand = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t *x = &s[16 * q];
+          float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+          float d = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+          a = max3(a, __uint_as_float(x[6]), __uint_as_float(x[7]));
+          d = max3(d, __uint_as_float(x[8]), __uint_as_float(x[9]));
+          a = max3(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
+          d = max3(d, __uint_as_float(x[12]), __uint_as_float(x[13]));
+          a = max3(a, __uint_as_float(x[14]), __uint_as_float(x[15]));
+          m_cand = fmaxf(m_cand, fmaxf(a, d) * cg[q]);
+        }
+        const bool grow = m_cand > m_run + kChunkTau;
+        const float m_new = grow ? m_cand : m_run;
+        const float fac = grow ? ex2_approx(m_run - m_new) : 1.0f;  // 0 on the first tile
+        m_run = m_new;
+        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+        const float p_max = ex2_approx(m_cand - m_use);
+        const float p_max_err = round_to_f16(p_max) - p_max;
+        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        uint64_t la = 0, lb = 0;
+        uint32_t pk[64];
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const uint64_t c2 = f2_pack(cg[i >> 3], cg[i >> 3]);
+          float x0, x1, x2, x3;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2,
+                           nm2),
+                    x0, x1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])),
+                           c2, nm2),
+                    x2, x3);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+          pk[i] = pack_f16x2(p0, p1);
+          pk[i + 1] = pack_f16x2(p2, p3);
+          la = f2_add(la, f2_pack(p0, p1));
+          lb = f2_add(lb, f2_pack(p2, p3));
+        }
+        tmem_st_32x32b_x32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+        tmem_st_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        // the value tile this step multiplies, and its exponent
+        if (!mbar_wait(&sb.v_ready[idx % C::kV16s], (idx / C::kV16s) & 1, abort_flag)) {
+          chunk_abort(sb, p.err);
+          goto done;
+        }
+        const int e_j = sb.v_exp[idx % C::kV16s];
+        const float ofac = j == 0 || e_j == e_cur ? fac : fac * exp2i(max(e_j - e_cur, -126));
+        e_cur = e_j;
+        if (j > 0 && __any_sync(0xffffffffu, ofac != 1.0f)) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              reg_barrier(o[i]);
+              reg_barrier(o[i + 1]);
+              float a, d;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                               f2_pack(ofac, ofac)),
+                        a, d);
+              o[i] = __float_as_uint(a);
+              o[i + 1] = __float_as_uint(d);
+            }
+            tmem_st_32x32b_x32(tO + c0, o);
+          }
+        }
+        {
+          float a0, a1;
+          f2_unpack(f2_add(la, lb), a0, a1);
+          l_run = l_run * fac + (a0 + a1);
+          lc_run = lc_run * fac + p_max_err;
+        }
+        if (j == n_t - 1) {
+          sb.m_fin[part & 1][t][row] = m_run;
+          sb.l_fin[part & 1][t][row] = l_run;
+          sb.lc_fin[part & 1][t][row] = lc_run;
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sb.p_full[t]);
+          if (j == n_t - 1) mbar_arrive(&sb.fin_full[part & 1][t]);
+        }
+      }
+      ++part;
+      step0 += run.n;
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ value conversion + epilogue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
+    const int cw = warp - 8;
+    const int row = cw * 32 + lane;  // epilogue: row == TMEM lane
+    const uint32_t lane_off = (uint32_t)(cw * 32) << 16;
+    // conversion: eight lanes take rows x and x ^ 5 of eight, four pieces each:
+    // neither the reads nor the writes of the swizzled tiles meet in a bank
+    const int crow = (lane >> 3) ^ ((lane & 4) ? 5 : 0), cpiece = lane & 3;
+    uint32_t step0 = 0, segs = 0;
+    uint32_t part[2] = {0, 0};
+    // the segment whose epilogue is pending
+    bool pend = false, pwhole = false;
+    int pb = 0, ph = 0, pmb = 0, pn[2] = {0, 0}, pe[2] = {0, 0}, prows = 0, plen = 0, pseg = 0;
+    while (true) {
+      const bool have = run.next(p);
+      const int n = have ? run.n : 0;
+      int e_run = 0, e_max = kKv8ExpMin, e_t0 = 0, e_t1 = 0;
+      for (int j = 0; j <= n; ++j) {
+        if (pend && (j == 1 || !have)) {
+          // every converter warp has seen the segment's value codes
+          if (!mbar_wait(&sb.conv_bar, (segs - 1) & 1, abort_flag)) {
+            chunk_abort(sb, p.err);
+            goto done;
+          }
+          const int par = (segs - 1) & 7;
+          const bool nan = sb.nan_any[par] != 0;
+          // the segment before is read by every converter warp: its slot starts anew
+          sb.nan_pos[(par + 7) & 7][row] = 0x7fffffff;
+          if (cw == 0 && lane == 0) sb.nan_any[(par + 7) & 7] = 0;
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            if (pn[t] == 0) continue;
+            const uint32_t pc = part[t]++;
+            if (!mbar_wait(&sb.fin_full[pc & 1][t], (pc >> 1) & 1, abort_flag) ||
+                !mbar_wait(&sb.o_full[t], pc & 1, abort_flag)) {
+              chunk_abort(sb, p.err);
+              goto done;
+            }
+            tc_fence_after_sync();
+            const float m = sb.m_fin[pc & 1][t][row];
+            const float l = sb.l_fin[pc & 1][t][row];
+            float oscale = exp2i(-pe[t]) / (l + sb.lc_fin[pc & 1][t][row]);
+            if (l == 0.f) oscale = 0.f;  // no position seen
+            const float lse =
+                l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994531f;
+            const int r = pmb * kChunkRows + t * 128 + row;
+            const bool ok = r < prows * p.G;
+            const int i = ok ? r / p.G : 0;
+            const int see = ok ? row_sees(p, i, plen, prows) : 0;
+            const uint32_t tO = tmem + lane_off + (t ? C::kColO1 : C::kColO0);
+            const long long orow =
+                ((long long)pb * p.H + ph * p.G + (ok ? r - i * p.G : 0)) * p.Nq + i;
+            float *part_row = p.part + (((size_t)blockIdx.x * 2 + (pseg > 0)) * kChunkRows +
+                                        t * 128 + row) * (D + 4);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tO + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                reg_barrier(o[k]);
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * oscale);
+              }
+              if (l == 0.f) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = 0;
+              }
+              if (nan) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (sb.nan_pos[par][c0 + k] < see) o[k] = 0x7fc00000u;
+              }
+              if (ok && pwhole) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + c0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  dst[k] = make_uint4(
+                      pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                      pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                      pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                      pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+              } else if (ok) {
+                uint4 *dst = reinterpret_cast<uint4 *>(part_row + c0);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              }
+            }
+            if (ok) {
+              if (pwhole)
+                p.lse[orow] = lse;
+              else
+                part_row[D] = lse;
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sb.o_free[t]);
+          }
+          pend = false;
+        }
+        if (j == n) break;
+        // Convert one value tile.
+        const uint32_t idx = step0 + j;
+        const uint32_t vs = idx % C::kVs, ws = idx % C::kV16s;
+        if (!mbar_wait(&sb.v_full[vs], (idx / C::kVs) & 1, abort_flag) ||
+            (idx >= (uint32_t)C::kV16s &&
+             !mbar_wait(&sb.v_free[ws], (idx / C::kV16s - 1) & 1, abort_flag))) {
+          chunk_abort(sb, p.err);
+          goto done;
+        }
+        const int valid = sb.k_valid[idx & 7];
+        const int k0 = (run.j0 + j) * 128;
+        {
+          // (runs that could not be read carry the least exponent)
+          int e8 = sb.v_exp8[idx & 7][lane & 7];
+          e_max = max(e_max, __reduce_max_sync(0xffffffffu, e8));
+        }
+        e_run = kChunkLift - e_max;
+        const uint8_t *raw = smem + C::kOffV + vs * C::kRaw;
+        uint8_t *dst = smem + C::kOffV16 + ws * C::kV16;
+        const int par = segs & 7;
+        const bool edge = valid != 0xff || k0 + 128 > run.sseq.len;
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tr = cw * 32 + i * 8 + crow;  // row of the tile
+          const float fs = exp2i(max(sb.v_exp8[idx & 7][tr >> 4] + e_run, -126));
+          const uint32_t f2 = pack_f16x2(fs, fs);
+#pragma unroll
+          for (int hc = 0; hc < D / 64; ++hc) {
+            const int pc = hc * 4 + cpiece;
+            uint4 w;
+            if constexpr (D == 128)
+              w = *reinterpret_cast<const uint4 *>(raw + tr * 128 + ((pc ^ (tr & 7)) << 4));
+            else
+              w = *reinterpret_cast<const uint4 *>(raw + tr * 64 + ((pc ^ ((tr >> 1) & 3)) << 4));
+            uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            if (edge && (!(valid >> (tr >> 4) & 1) || k0 + tr >= run.sseq.len)) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) x[y] = 0;
+            }
+            uint32_t any = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) any |= (x[y] & 0x7f7f7f7fu) + 0x01010101u;
+            if (any & 0x80808080u) {  // rare: a NaN code
+              odd = 1;
+              for (int y = 0; y < 16; ++y) {
+                const uint32_t code = x[y >> 2] >> (8 * (y & 3)) & 0x7fu;
+                if (code == 0x7fu) {
+                  atomicMin(&sb.nan_pos[par][pc * 16 + y], k0 + tr);
+                }
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t hit = ((x[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                x[y] &= ~((hit >> 7) * 0xffu);
+              }
+            }
+            uint32_t o[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              e4m3x4_to_f16x2x2(x[y], o[2 * y], o[2 * y + 1]);
+              asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[2 * y]) : "r"(f2));
+              asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[2 * y + 1]) : "r"(f2));
+            }
+            uint8_t *line = dst + hc * 16384 + tr * 128;
+            *reinterpret_cast<uint4 *>(line + (((2 * cpiece) ^ (tr & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(line + (((2 * cpiece + 1) ^ (tr & 7)) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        if (odd) sb.nan_any[par] = 1;
+        fence_proxy_async_smem();
+        if (cw == 0 && lane == 0) sb.v_exp[ws] = e_run;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sb.v_ready[ws]);
+          mbar_arrive(&sb.v_empty[vs]);
+        }
+        if (j == run.n0 - 1) e_t0 = e_run;
+        if (j == run.n1 - 1) e_t1 = e_run;
+      }
+      if (!have) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.conv_bar);
+      pend = true;
+      pwhole = run.whole;
+      pb = run.sb;
+      ph = run.sh;
+      pmb = run.smb;
+      pn[0] = run.n0;
+      pn[1] = run.n1;
+      pe[0] = e_t0;
+      pe[1] = e_t1;
+      prows = run.sseq.rows;
+      plen = run.sseq.len;
+      pseg = (int)segs;
+      ++segs;
+      step0 += n;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
+    if (warp == 12 && lane == 0) {
+      // ---------------------------------------------------------- tensor-core issue
+      // Step j: P0 V_{j-1}, S0 = Q0 K_j^T, then P1 V_{j-1}, S1 = Q1 K_j^T, so each
+      // tile's softmax works while the other tile's products run.
+      constexpr uint32_t idS = idesc_e4m3_f32(128, 128);
+      constexpr uint32_t idO = idesc_f32acc(false, 128, D, false, true);
+      const uint32_t hi128 = sdesc_sw128_hi(1024);
+      const uint32_t hik = D == 128 ? sdesc_sw128_hi(1024) : sdesc_sw64_hi(512);
+      const uint32_t q_lo0 = sdesc_sw128_lo(smem_addr(smem), 16);
+      const uint32_t k_lo0 = sdesc_sw128_lo(smem_addr(smem + C::kOffK), 16);
+      const uint32_t v_lo0 = sdesc_sw128_lo(smem_addr(smem + C::kOffV16), 16384);
+      uint32_t p_phase[2] = {0, 0};
+      uint32_t part[2] = {0, 0};
+      uint32_t step0 = 0;
+      while (run.next(p)) {
+        const int n = run.n;
+#pragma unroll 1
+        for (int j = 0; j <= n; ++j) {
+          const uint32_t kidx = step0 + j, vidx = kidx - 1;
+          const uint32_t ks = kidx % C::kKs, ws = vidx % C::kV16s;
+          bool k_ready = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int n_t = t ? run.n1 : run.n0;
+            const bool do_pv = j >= 1 && j <= n_t;
+            const bool do_s = j < n_t;
+            const uint32_t tS = tmem + (t ? C::kColS1 : C::kColS0);
+            const uint32_t tO = tmem + (t ? C::kColO1 : C::kColO0);
+            if (do_pv) {
+              // (P is signalled only once V_{j-1} is converted)
+              if ((j == 1 && part[t] > 0 &&
+                   !mbar_wait(&sb.o_free[t], (part[t] - 1) & 1, abort_flag)) ||
+                  !mbar_wait(&sb.p_full[t], p_phase[t], abort_flag)) {
+                chunk_abort(sb, p.err);
+                goto mma_exit;
+              }
+              p_phase[t] ^= 1;
+            }
+            if (do_s) {
+              if ((j == 0 && !mbar_wait(&sb.q_full[t], part[t] & 1, abort_flag)) ||
+                  (!k_ready && !mbar_wait(&sb.k_full[ks], (kidx / C::kKs) & 1, abort_flag))) {
+                chunk_abort(sb, p.err);
+                goto mma_exit;
+              }
+              k_ready = true;
+            }
+            tc_fence_after_sync();
+            if (do_pv) {
+              const uint32_t v_lo = v_lo0 + ws * (C::kV16 >> 4);
+              umma_ts_w_rt(tO, tS, v_lo, hi128, idO, j > 1 ? 1u : 0u);
+#pragma unroll
+              for (int kk = 1; kk < 8; ++kk)
+                umma_ts_w<1>(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), hi128, idO);
+            }
+            if (do_s) {
+              const uint32_t a = q_lo0 + t * (C::kQTile >> 4), bk = k_lo0 + ks * (C::kRaw >> 4);
+              // 32 codes a product; hi, then lo
+              umma_f8_ss<0>(tS, a, hi128, bk, hik, idS);
+#pragma unroll
+              for (int kk = 1; kk < D / 16; ++kk) {
+                const int x = kk % (D / 32);
+                const uint32_t off =
+                    D == 128 ? (kk / 4) * (16384 >> 4) + x * 2 : (uint32_t)kk * 2;
+                umma_f8_ss<1>(tS, a + off, hi128, bk + x * 2, hik, idS);
+              }
+              umma_commit(&sb.s_full[t]);
+            }
+            if (do_pv && j == n_t) {
+              umma_commit(&sb.o_full[t]);
+              ++part[t];
+            }
+          }
+          if (j < n) umma_commit(&sb.k_empty[ks]);
+          if (j >= 1) umma_commit(&sb.v_free[ws]);
+        }
+        step0 += n;
+      }
+    mma_exit:
+      // every product must finish before the tensor memory is freed
+      umma_commit(&sb.mma_done);
+      {
+        int never = 0;
+        mbar_wait(&sb.mma_done, 0, &never);
+      }
+    }
+    if (warp == 14) {
+      // ---------------------------------------------------------- TMA, a lane a page
+      uint32_t idx = 0;  // steps loaded
+      const int pages = 128 >> p.page_log2;  // of a tile
+      bool gone = false;
+      while (!gone && run.next(p)) {
+        const int len = run.sseq.len;
+        // this lane's page of tile x: its index, or -1
+        auto fetch = [&](int x) -> int {
+          const int t = x * 128 + (lane << p.page_log2);
+          if (lane >= pages || t >= len) return -1;
+          const int id = p.table[kv8_table_offset(g, run.sb, t >> p.page_log2)];
+          if (kv8_page_ok(g, id)) return id;
+          atomicCAS(p.err, 0, kDevErrIndex);
+          return -1;
+        };
+        int id = fetch(run.j0);
+        int id_next = run.n > 1 ? fetch(run.j0 + 1) : -1;
+        int ke = id >= 0 ? p.ke[id * g.Hkv + run.sh] : 0;
+        int ve = id >= 0 ? p.ve[id * g.Hkv + run.sh] : kKv8ExpMin;
+        for (int j = 0; j < run.n; ++j, ++idx) {
+          const uint32_t ks = idx % C::kKs, vs = idx % C::kVs;
+          // the next tile's exponents, and the one after's pages
+          const int ke1 = id_next >= 0 ? p.ke[id_next * g.Hkv + run.sh] : 0;
+          const int ve1 = id_next >= 0 ? p.ve[id_next * g.Hkv + run.sh] : kKv8ExpMin;
+          const int id2 = j + 2 < run.n ? fetch(run.j0 + j + 2) : -1;
+          int ok = 1;
+          if (lane == 0 && idx >= (uint32_t)C::kKs)
+            ok = mbar_wait(&sb.k_empty[ks], (idx / C::kKs - 1) & 1, abort_flag);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            if (lane == 0) chunk_abort(sb, p.err);
+            gone = true;
+            break;
+          }
+          const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
+          const uint32_t bytes = __popc(have) * g.page * D;
+          // eight runs of 16 positions, whatever the page
+          {
+            const int src = (lane & 7) >> (p.page_log2 - 4);
+            const int kr = __shfl_sync(0xffffffffu, ke, src), vr = __shfl_sync(0xffffffffu, ve, src);
+            if (lane < 8) {
+              sb.k_scale[idx & 7][lane] = exp2i(max(kr, -126));
+              sb.v_exp8[idx & 7][lane] = vr;
+            }
+            const uint32_t bits = __ballot_sync(0xffffffffu, lane < 8 && (have >> src & 1));
+            if (lane == 0) sb.k_valid[idx & 7] = (int)bits;
+          }
+          __syncwarp();
+          const int y = (id * g.Hkv + run.sh) << p.page_log2;
+          if (lane == 0) mbar_arrive_expect_tx(&sb.k_full[ks], bytes);
+          __syncwarp();
+          if (id >= 0)
+            tma_load_2d(smem + C::kOffK + ks * C::kRaw + (lane << p.page_log2) * D, &tm_k,
+                        &sb.k_full[ks], 0, y);
+          if (lane == 0 && idx >= (uint32_t)C::kVs)
+            ok = mbar_wait(&sb.v_empty[vs], (idx / C::kVs - 1) & 1, abort_flag);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            if (lane == 0) chunk_abort(sb, p.err);
+            gone = true;
+            // the key tile of this step is in flight: wait for it below
+            int never = 0;
+            if (lane == 0) mbar_wait(&sb.k_full[ks], (idx / C::kKs) & 1, &never);
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&sb.v_full[vs], bytes);
+          __syncwarp();
+          if (id >= 0)
+            tma_load_2d(smem + C::kOffV + vs * C::kRaw + (lane << p.page_log2) * D, &tm_v,
+                        &sb.v_full[vs], 0, y);
+          id = id_next;
+          ke = ke1;
+          ve = ve1;
+          id_next = id2;
+        }
+      }
+      // wait for the copies still in flight (all consumed on the normal path)
+      if (lane == 0) {
+        int never = 0;
+        for (uint32_t s = 0; s < (uint32_t)C::kKs && s < idx; ++s) {
+          const uint32_t last = idx - 1 - ((idx - 1 - s) % C::kKs);
+          mbar_wait(&sb.k_full[s], (last / C::kKs) & 1, &never);
+        }
+        for (uint32_t s = 0; s < (uint32_t)C::kVs && s < idx; ++s) {
+          const uint32_t last = idx - 1 - ((idx - 1 - s) % C::kVs);
+          mbar_wait(&sb.v_full[s], (last / C::kVs) & 1, &never);
+        }
+      }
+    }
+  }
+done:
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 12) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the runs' partial results (O / l and LSE of a run): a warp a row,
+// eight rows a block.  grid: (ceil(Nq * G / 8), Hkv, B)
+template <int D>
+__global__ void __launch_bounds__(256)
+    tk_kv8_chunk_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const ChunkSeq s = chunk_seq(p, b);
+  const int mb = r / kChunkRows;
+  // steps of the head's units before this row's, and of all of them
+  long long before = 0, all = 0;
+  for (int x = lane; x < s.units; x += 32) {
+    const int c = chunk_cost(p, s, x);
+    all += c;
+    if (x < mb) before += c;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+  }
+  grid_wait();  // every block waits: this launch's end means the end of the one before too
+  if (r >= s.rows * p.G) return;
+  const long long share = max(1LL, (p.prefix[p.B] + p.ctas - 1) / p.ctas);
+  const long long s0 = p.prefix[b] + h * all + before;
+  const int cost = chunk_cost(p, s, mb);
+  const int c0 = (int)(s0 / share), c1 = (int)((s0 + cost - 1) / share);
+  if (c0 == c1) return;
+  const int t = (r / 128) & 1;
+  const int tiles = chunk_tiles(p, mb * kChunkRows + t * 128, s.len, s.rows);
+  const size_t slot = (size_t)kChunkRows * (D + 4);
+  const float *base = p.part + (size_t)(r % kChunkRows) * (D + 4);
+  const int first0 = c0 * share == s0 ? 0 : 1;
+  constexpr int kPer = D / 32;
+  // runs that hold no key tile of this row's tile wrote nothing for it
+  const int c_end = min(c1, (int)((s0 + tiles - 1) / share));
+  float mx = -INFINITY;
+  for (int c = c0; c <= c_end; ++c)
+    mx = fmaxf(mx, base[((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot + D]);
+  const float mu = mx == -INFINITY ? 0.f : mx;
+  float z = 0.f, acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+  for (int c = c0; c <= c_end; ++c) {
+    const float *d = base + ((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot;
+    const float w = expf(d[D] - mu);
+    z += w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, d[lane * kPer + i], acc[i]);
+  }
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  const int i = r / p.G;
+  const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
+  uint32_t pk[kPer / 2];
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k) pk[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * kPer);
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k) dst[k] = pk[k];
+  if (lane == 0) p.lse[orow] = z == 0.f ? -INFINITY : mu + logf(z);
+}
+
+}  // namespace tkattn

@@ -8,7 +8,7 @@
 // causal mask up to the row's own position).
 //
 // Bound by reading the cache once, so the kernel streams it:
-//  - Work is the list of (sequence, head, row tile, 64-position unit); every
+//  - Work is the list of (sequence, head, 64-position unit); every
 //    CTA takes an equal run of it, whatever the lengths (they live on the
 //    device; each CTA finds its run by a scan over the sequences).  A run that
 //    starts or ends inside a segment leaves a partial result (running maximum,
@@ -70,11 +70,11 @@ struct Kv8AttnParams {
   int B, H, G, Nq;  // G = H / Hkv
   int causal;
   float scale_log2;  // scale * log2(e)
-  int tile_rows;     // query rows of a tile
-  int row_tiles;     // ceil(Nq * G / tile_rows)
+  int tile_rows;     // (few rows) 8 or 16, at least Nq * G
   int ctas;          // runs the work is cut into
   int *err;
-  float *part;       // [ctas, 2, rows of a tile, D + 4]
+  float *part;       // [ctas, 2, rows of a tile or unit, D + 4]
+  long long *prefix;  // (many rows) the work before each sequence, the total last
 };
 
 constexpr int kDecWarps = 4;
@@ -128,15 +128,17 @@ struct Kv8Place {
   int b;
 };
 
-// Total work, and the sequence in which run `run` starts (b = B when past the
-// end), or with find_b >= 0 the units before sequence find_b.  Whole block;
-// ends with a barrier.
-__device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, int unit, long long segs,
-                                         int run, int find_b, Kv8Place *out, long long *red) {
+// Total work (cost(b) over the sequences), and the sequence in which run `run`
+// starts (b = B when past the end), or with find_b >= 0 the work before
+// sequence find_b.  With `prefix` the work before each sequence is written
+// there, the total last.  Whole block; ends with a barrier.
+template <typename Cost>
+__device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, Cost cost, int run, int find_b,
+                                         Kv8Place *out, long long *red, long long *prefix) {
   const int nthr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long v0 = threadIdx.x < p.B ? seq_units(p, threadIdx.x, unit) * segs : 0;
+  const long long v0 = (int)threadIdx.x < p.B ? cost(threadIdx.x) : 0;
   long long sum = v0;
-  for (int b = threadIdx.x + nthr; b < p.B; b += nthr) sum += seq_units(p, b, unit) * segs;
+  for (int b = threadIdx.x + nthr; b < p.B; b += nthr) sum += cost(b);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0) red[warp] = sum;
@@ -144,13 +146,16 @@ __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, int unit, long 
   __syncthreads();
   long long total = 0;
   for (int w = 0; w < nthr / 32; ++w) total += red[w];
-  if (threadIdx.x == 0) out->total = total;
+  if (threadIdx.x == 0) {
+    out->total = total;
+    if (prefix) prefix[p.B] = total;
+  }
   const long long u = run * max(1LL, (total + p.ctas - 1) / p.ctas);
   __syncthreads();
   long long carry = 0;
   for (int base = 0; base < p.B; base += nthr) {
     const int b = base + threadIdx.x;
-    const long long v = base == 0 ? v0 : b < p.B ? seq_units(p, b, unit) * segs : 0;
+    const long long v = base == 0 ? v0 : b < p.B ? cost(b) : 0;
     long long inc = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -163,9 +168,12 @@ __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, int unit, long 
     for (int w = 0; w < warp; ++w) before += red[w];
     for (int w = 0; w < nthr / 32; ++w) carry += red[w];
     const long long lo = before + inc - v;
-    if (b < p.B && (find_b >= 0 ? b == find_b : (u >= lo && u < lo + v))) {
-      out->b = b;
-      out->prefix = lo;
+    if (b < p.B) {
+      if (prefix) prefix[b] = lo;
+      if (find_b >= 0 ? b == find_b : (u >= lo && u < lo + v)) {
+        out->b = b;
+        out->prefix = lo;
+      }
     }
     __syncthreads();
   }
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q8 = lane >> 2, c4 = lane & 3;
   const Kv8Geom &g = p.g;
-  const int segs = g.Hkv * p.row_tiles;
+  const int segs = g.Hkv;  // segments of a sequence
   float *merge_o = reinterpret_cast<float *>(smem + C::kRingBytes);
   float *merge_s = merge_o + kDecWarps * C::kRows * C::kRowStride;  // m, M, l of each warp's rows
 
@@ -267,7 +275,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     }
     if (bad) atomicCAS(p.err, 0, kDevErrIndex);
   }
-  kv8_scan(p, kDecUnit, segs, blockIdx.x, -1, &place, red);
+  kv8_scan(
+      p, [&](int b) { return (long long)seq_units(p, b, kDecUnit) * segs; }, blockIdx.x, -1,
+      &place, red, nullptr);
   const long long share = max(1LL, (place.total + p.ctas - 1) / p.ctas);
   const long long u0 = blockIdx.x * share;
   if (u0 >= place.total) return;
@@ -313,7 +323,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       cp_async_commit();
       return -1;
     }
-    const int h = p.row_tiles == 1 ? prod.seg : prod.seg / p.row_tiles;
+    const int h = prod.seg;
     const int t = prod.unit * kDecUnit + warp * 16;
     const int eoff = id * g.Hkv + h;  // (the host bounds num_pages * Hkv)
     const long long off = (long long)eoff * (g.page * D) + (t & (g.page - 1)) * D;
@@ -351,8 +361,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   int step = 0, seg_index = 0, stage = 0;
   while (step < nsteps) {
     // ---------------------------------------------------------- one segment
-    const int b = cons.b, h = cons.seg / p.row_tiles;
-    const int rt = cons.seg - h * p.row_tiles;
+    const int b = cons.b, h = cons.seg;
     const int len = cons.len;
     const int n_here = min(cons.units - cons.unit, nsteps - step);
     const bool whole = cons.unit == 0 && n_here == cons.units;
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     int vis_min = len;
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
-      const int r = rt * C::kRows + 8 * t + q8;
+      const int r = 8 * t + q8;
       const bool on = r < r_end;
       const int i = r / p.G;
       const __nv_bfloat16 *src =
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int rx = rt * C::kRows + 8 * t + 2 * c4 + x;
+        const int rx = 8 * t + 2 * c4 + x;
         vis[t][x] = rx < r_end ? row_sees(p, rx / p.G, len, rows) : 0;
         vis_min = min(vis_min, rx < r_end ? vis[t][x] : len);
         f[t][x] = __shfl_sync(0xffffffffu, fr, (2 * c4 + x) * 4);
@@ -438,7 +447,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       stage = stage == kStages - 1 ? 0 : stage + 1;
       const int t0 = (cons.unit + n) * kDecUnit + warp * 16;
       if (none) continue;  // no positions of this warp (warp-uniform)
-      const float fk = exp2i(ke);
+      const float fk = exp2i(max(ke, -126));
       const float ev = (float)ve;
 
       // S^T = K Q^T: 16 positions x 8 rows a tile; s[t][0, 1]: position q8,
@@ -557,9 +566,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
         }
         if (__any_sync(0xffffffffu, odd)) {
           // query by query, without the positions that one does not see
-          const int i_lo = rt * C::kRows / p.G;
-          const int i_hi = min(rows - 1, (rt * C::kRows + C::kRows - 1) / p.G);
-          for (int i = i_lo; i <= i_hi; ++i) {
+          for (int i = 0; i < rows; ++i) {
             const int see = row_sees(p, i, len, rows);
             uint32_t z[4][kVw];
 #pragma unroll
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
                 z[k][y] = t0 + 2 * c4 + (k & 1) + (k >> 1) * 8 < see ? w[k][y] : 0u;
 #pragma unroll
             for (int t = 0; t < kNT; ++t) {
-              const int ra = rt * C::kRows + 8 * t + 2 * c4;
+              const int ra = 8 * t + 2 * c4;
               const bool on0 = ra / p.G == i, on1 = (ra + 1) / p.G == i;
 #pragma unroll
               for (int j = 0; j < kSteps; ++j) {
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       constexpr int kPer = kDecThreads / C::kRows;  // threads of a row
       constexpr int kCols = D / kPer;               // columns of a thread
       const int row = threadIdx.x / kPer, col = (threadIdx.x % kPer) * kCols;
-      const int r = rt * C::kRows + row;
+      const int r = row;
       if (r < r_end) {
         float mm = kDecNone, mmo = kDecNone, ll = 0.f;
         float4 st[kDecWarps];
@@ -693,30 +700,30 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
 }
 
 // Merge of the runs' partial results: one block (a thread a column) for each
-// (head and row tile, sequence, row).  Segments that one run held whole are
+// (head, sequence, row).  Segments that one run held whole are
 // already written.
 template <int D>
 __global__ void __launch_bounds__(D)
     tk_kv8_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
   __shared__ Kv8Place place;
   __shared__ long long red[4];
-  const int seg = blockIdx.x, b = blockIdx.y, row = blockIdx.z;
-  const int segs = p.g.Hkv * p.row_tiles;
-  const int h = seg / p.row_tiles, rt = seg - h * p.row_tiles;
+  const int h = blockIdx.x, b = blockIdx.y, r = blockIdx.z;
+  const int segs = p.g.Hkv;
   bool bad = false;
   const int rows = seq_rows(p, b, &bad);
-  const int r = rt * p.tile_rows + row;
-  kv8_scan(p, kDecUnit, segs, 0, b, &place, red);
+  kv8_scan(
+      p, [&](int b) { return (long long)seq_units(p, b, kDecUnit) * segs; }, 0, b, &place, red,
+      nullptr);
   const int units = seq_units(p, b, kDecUnit);
   const long long share = max(1LL, (place.total + p.ctas - 1) / p.ctas);
-  const long long s0 = place.prefix + (long long)seg * units;
+  const long long s0 = place.prefix + (long long)h * units;
   const int c0 = (int)(s0 / share), c1 = (int)((s0 + max(units, 1) - 1) / share);
   // All above reads only what the launch before leaves alone.  Every block
   // waits, so that this launch's end means the end of the one before too.
   grid_wait();
   if (r >= rows * p.G || c0 == c1) return;
   // run c0's partial is its first segment's only if it starts where the segment does
-  const float *base = p.part + (size_t)row * (D + 4);
+  const float *base = p.part + (size_t)r * (D + 4);
   const size_t slot = (size_t)p.tile_rows * (D + 4);
   const int first0 = c0 * share == s0 ? 0 : 1;
   auto at = [&](int c) { return base + ((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot; };
