@@ -324,7 +324,7 @@ extern "C" int tk_attn_fwd_kv8_check_args(const void *q, const void *k_cache, co
       ((uintptr_t)lengths | (uintptr_t)counts) & 3u)
     return TK_ATTN_ERR_UNSUPPORTED;
   const long long G = H / Hkv;
-  if (B > 65535 || (long long)Nq * G > (1LL << 30) ||
+  if (B > 65535 || Nq * G * G > 0x7fffffffLL ||
       (long long)Hkv * (((long long)Nq * G + 7) / 8) > 0x7fffffffLL ||
       (long long)B * H > 0x7fffffffLL)
     return TK_ATTN_ERR_UNSUPPORTED;
@@ -371,6 +371,7 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
   p.B = B;
   p.H = H;
   p.G = H / Hkv;
+  p.g_mul = p.G == 1 ? 0u : (unsigned)((1ull << 32) / p.G + 1);
   p.Nq = Nq;
   p.causal = causal != 0;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);

@@ -31,7 +31,9 @@
 //                   tile's queries (their last scores being in hand, no product
 //                   still reads them)
 //   warps 8-11      value conversion, and the epilogue
-//   warp 12         tensor-core issue; warp 14: TMA, a lane a page
+//   warp 12         tensor-core issue
+//   warps 13, 14    TMA loads of values and of keys, a lane a page
+//   warp 15         the run's segments, which the other roles read
 // A NaN value code would spread over a tile's rows through 0 * NaN: codes are
 // replaced by 0 and the first position of each column that held one is kept;
 // rows that see that position get NaN in that column.
@@ -64,13 +66,22 @@ struct ChunkCfg {
   static constexpr int kKs = D == 128 ? 3 : 4;           // key ring
   static constexpr int kVs = D == 128 ? 2 : 4;           // value ring
   static constexpr int kV16 = 128 * D * 2;               // a converted value tile
-  static constexpr int kV16s = 2;
+  static constexpr int kV16s = 2;  // (the issue loop flips between them)
   static constexpr int kOffK = 2 * kQTile;
   static constexpr int kOffV = kOffK + kKs * kRaw;
   static constexpr int kOffV16 = kOffV + kVs * kRaw;
   static constexpr int kSmem = kOffV16 + kV16s * kV16;
   static constexpr int kSmemAlloc = kSmem + 1024;  // + alignment slack
   static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+};
+
+// A segment: the part of one unit that lies in a CTA's run.
+struct ChunkSeg {
+  int b, h, mb;     // mb < 0: the run is over
+  int j0, n;        // its key tiles
+  int n0, n1;       // how many of them each tile of queries visits
+  int len, rows;    // of the sequence
+  int whole;        // the unit lies in this run alone
 };
 
 struct ChunkShared {
@@ -87,17 +98,20 @@ struct ChunkShared {
   uint64_t o_full[2];     // tile's last P V of a unit done  (commit)
   uint64_t o_free[2];     // epilogue has read O             (4 converter warps)
   uint64_t conv_bar;      // converter warps, once a unit    (4 converter warps)
+  uint64_t seg_full[4];   // segment posted                  (1)
+  uint64_t seg_empty[4];  // every role has read it          (15: 8 + 4 warps, issue, 2 loads)
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
   // run
   Kv8Place place;
   long long red[kChunkThreads / 32];
-  int start_h, start_mb, start_j;
+  ChunkSeg seg[4];
   // per step, eight deep: a slot is rewritten only when every reader is four steps on
   alignas(16) float k_scale[8][8];  // 2^ke of the tile's eight runs of 16 positions
   int k_valid[8];         // bit g: run g lies in a page that could be read
   int v_exp8[8][8];       // value exponents of the runs
+  int v_valid[8];         // as k_valid, for the values
   int v_exp[2];           // exponent the converted tile carries (6 - E)
   float m_fin[2][2][128], l_fin[2][2][128], lc_fin[2][2][128];  // [parity][tile][row]
   // eight segments deep: a converter warp is at most two tiles ahead of another
@@ -115,7 +129,7 @@ __device__ __forceinline__ void chunk_abort(ChunkShared &sb, int *err) {
 __device__ __forceinline__ int chunk_tiles(const Kv8AttnParams &p, int first, int len, int rows) {
   const int r_end = rows * p.G;
   if (first >= r_end) return 0;
-  const int i = min(first + 127, r_end - 1) / p.G;
+  const int i = row_query(p, min(first + 127, r_end - 1));
   return max(1, (row_sees(p, i, len, rows) + 127) / 128);
 }
 
@@ -137,52 +151,10 @@ __device__ __forceinline__ int chunk_cost(const Kv8AttnParams &p, const ChunkSeq
 __device__ __forceinline__ long long chunk_seq_cost(const Kv8AttnParams &p, int b) {
   const ChunkSeq s = chunk_seq(p, b);
   long long c = 0;
+#pragma unroll 1
   for (int mb = 0; mb < s.units; ++mb) c += chunk_cost(p, s, mb);
   return c;
 }
-
-// The CTA's run of steps, one segment (part of a unit) after another.
-struct ChunkRun {
-  int b, h, mb, j;  // next segment's unit and key tile
-  long long left;   // steps left in the run
-  ChunkSeq seq;
-  // the current segment
-  int sb, sh, smb, j0, n0, n1, n;
-  ChunkSeq sseq;
-  bool whole;
-
-  __device__ __forceinline__ bool next(const Kv8AttnParams &p) {
-    if (left == 0) return false;
-    const int t0 = chunk_tiles(p, mb * kChunkRows, seq.len, seq.rows);
-    const int t1 = chunk_tiles(p, mb * kChunkRows + 128, seq.len, seq.rows);
-    const int cost = max(t0, t1);
-    sb = b;
-    sh = h;
-    smb = mb;
-    sseq = seq;
-    j0 = j;
-    n = (int)min((long long)(cost - j), left);
-    n0 = min(max(t0 - j, 0), n);
-    n1 = min(max(t1 - j, 0), n);
-    whole = j == 0 && n == cost;
-    left -= n;
-    j += n;
-    if (j == cost) {
-      j = 0;
-      if (++mb == seq.units) {
-        mb = 0;
-        if (++h == p.g.Hkv) {
-          h = 0;
-          while (++b < p.B) {
-            seq = chunk_seq(p, b);
-            if (seq.units > 0) break;
-          }
-        }
-      }
-    }
-    return true;
-  }
-};
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int x, int y) {
@@ -228,20 +200,20 @@ __device__ __forceinline__ float chunk_queries(const Kv8AttnParams &p, int b, in
   const int l = lane % kLanes, sub = lane / kLanes;
   float mine = 1.f;
 #pragma unroll 1
-  for (int it0 = 0; it0 < kIts; it0 += 4) {
+  for (int it0 = 0; it0 < kIts; it0 += 2) {
     if (first + w * 32 + it0 * kPerIt >= r_end) break;  // no row left (warp-uniform)
-    uint4 v[4];
+    uint4 v[2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       const int r = first + w * 32 + (it0 + u) * kPerIt + sub;
-      const int i = r / p.G;
+      const int i = row_query(p, r);
       v[u] = r < r_end ? *reinterpret_cast<const uint4 *>(
                              p.q + (((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i) * D +
                              l * 8)
                        : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       const int row = w * 32 + (it0 + u) * kPerIt + sub;  // row of the tile
       const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
       uint32_t am = 0;
@@ -291,6 +263,111 @@ __device__ __forceinline__ float chunk_queries(const Kv8AttnParams &p, int b, in
   return mine;
 }
 
+// The x-th segment of the run, as a role reads it; false if the wait was
+// abandoned.  Whole warp (or the one thread of a role that has no more).
+__device__ __forceinline__ bool chunk_next(ChunkShared &sb, uint32_t x, bool arrive,
+                                           volatile int *abort_flag, ChunkSeg &out) {
+  if (!mbar_wait(&sb.seg_full[x & 3], (x >> 2) & 1, abort_flag)) return false;
+  out = sb.seg[x & 3];
+  if (arrive) mbar_arrive(&sb.seg_empty[x & 3]);
+  return true;
+}
+
+// The loads of the run's key tiles or (kV) value tiles, a lane a page, and what
+// the other roles have to know of each: which pages could be read, and their
+// factors.  One body for both warps: the code streams of an SM's roles share its
+// instruction fetch, which bounds this kernel when they are long.  Page numbers and exponents are fetched 32 pages at a time, one batch
+// ahead of their use.
+template <int D>
+__device__ __forceinline__ void chunk_load(const Kv8AttnParams &p, bool kV, const CUtensorMap *map,
+                                           ChunkShared &sb, uint8_t *ring, int lane,
+                                           volatile int *abort_flag) {
+  using C = ChunkCfg<D>;
+  const uint32_t kRing = kV ? C::kVs : C::kKs;
+  uint64_t *full = kV ? sb.v_full : sb.k_full, *empty = kV ? sb.v_empty : sb.k_empty;
+  const int8_t *exps = kV ? p.ve : p.ke;
+  const Kv8Geom &g = p.g;
+  const int pages = 128 >> p.page_log2;  // of a tile
+  const int batch = 32 / pages;          // tiles of 32 pages
+  uint32_t idx = 0;                      // steps loaded
+  uint32_t st = 0, turn = 0;             // ring slot of step idx, parity of its use
+  bool gone = false;
+#pragma unroll 1
+  for (uint32_t sx = 0; !gone; ++sx) {
+    ChunkSeg sg;
+    if (!chunk_next(sb, sx, lane == 0, abort_flag, sg)) {
+      if (lane == 0) chunk_abort(sb, p.err);
+      break;
+    }
+    if (sg.mb < 0) break;
+    // lane's page of the batch that starts at tile x of the segment, or -1
+    auto fetch = [&](int x) -> int {
+      const long long t = (long long)(sg.j0 + x) * 128 + ((long long)lane << p.page_log2);
+      if (x >= sg.n || t >= sg.len || t >= (long long)(sg.j0 + sg.n) * 128) return -1;
+      const int id = p.table[kv8_table_offset(g, sg.b, (int)(t >> p.page_log2))];
+      if (kv8_page_ok(g, id)) return id;
+      if (!kV) atomicCAS(p.err, 0, kDevErrIndex);
+      return -1;
+    };
+    auto fetch_exp = [&](int id) -> int {
+      return id >= 0 ? (int)exps[id * g.Hkv + sg.h] : (kV ? kKv8ExpMin : 0);
+    };
+    int id = fetch(0), ex = fetch_exp(id);
+    int id_next = fetch(batch), ex_next = 0;
+#pragma unroll 1
+    for (int j = 0; j < sg.n; ++j, ++idx) {
+      const int x = j & (batch - 1);  // tile of the batch
+      if (x == 0 && j > 0) {
+        id = id_next;
+        ex = batch > 1 ? ex_next : fetch_exp(id);
+        id_next = fetch(j + batch);
+      }
+      if (x == (batch > 1 ? 1 : 0)) ex_next = fetch_exp(id_next);
+      int ok = 1;
+      if (lane == 0 && idx >= kRing) ok = mbar_wait(&empty[st], turn ^ 1, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        if (lane == 0) chunk_abort(sb, p.err);
+        gone = true;
+        break;
+      }
+      // eight runs of 16 positions, whatever the page
+      const int src = x * pages + ((lane & 7) >> (p.page_log2 - 4));
+      const int er = __shfl_sync(0xffffffffu, ex, src);
+      const int mine = __shfl_sync(0xffffffffu, id, x * pages + (lane & (pages - 1)));
+      const uint32_t have = __ballot_sync(0xffffffffu, lane < pages && mine >= 0);
+      const uint32_t bits = __ballot_sync(
+          0xffffffffu, lane < 8 && (have >> ((lane & 7) >> (p.page_log2 - 4)) & 1));
+      if (kV) {
+        if (lane < 8) sb.v_exp8[idx & 7][lane] = er;
+        if (lane == 0) sb.v_valid[idx & 7] = (int)bits;
+      } else {
+        if (lane < 8) sb.k_scale[idx & 7][lane] = exp2i(max(er, -126));
+        if (lane == 0) sb.k_valid[idx & 7] = (int)bits;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(have) * g.page * D);
+      __syncwarp();
+      if (lane < pages && mine >= 0)
+        tma_load_2d(ring + st * C::kRaw + (lane << p.page_log2) * D, map, &full[st], 0,
+                    (mine * g.Hkv + sg.h) << p.page_log2);
+      if (++st == kRing) {
+        st = 0;
+        turn ^= 1;
+      }
+    }
+  }
+  // wait for the copies still in flight (all consumed on the normal path)
+  if (lane == 0) {
+    int never = 0;
+#pragma unroll 1
+    for (uint32_t s = 0; s < kRing && s < idx; ++s) {
+      const uint32_t last = idx - 1 - ((idx - 1 - s) % kRing);
+      mbar_wait(&full[s], (last / kRing) & 1, &never);
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     tk_kv8_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -325,6 +402,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sb.v_full[s], 1);
       mbar_init(&sb.v_empty[s], 4);
     }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sb.seg_full[s], 1);
+      mbar_init(&sb.seg_empty[s], 15);
+    }
     mbar_init(&sb.conv_bar, 4);
     mbar_init(&sb.mma_done, 1);
     sb.abort = 0;
@@ -343,6 +424,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
   if (blockIdx.x == 0) {  // report what is out of range, once
     bool bad = false;
+#pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kChunkThreads) {
       seq_len(p, b, &bad);
       seq_rows(p, b, &bad);
@@ -352,39 +434,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   kv8_scan(
       p, [&](int b) { return chunk_seq_cost(p, b) * p.g.Hkv; }, blockIdx.x, -1, &sb.place, sb.red,
       blockIdx.x == 0 ? p.prefix : nullptr);
-  const long long share = max(1LL, (sb.place.total + p.ctas - 1) / p.ctas);
-  const long long u0 = blockIdx.x * share;
-  const long long steps = min(share, sb.place.total - u0);
-  if (threadIdx.x == 0 && steps > 0) {
-    const long long l = u0 - sb.place.prefix;
-    const ChunkSeq s = chunk_seq(p, sb.place.b);
-    const long long per_head = chunk_seq_cost(p, sb.place.b);
-    sb.start_h = (int)(l / per_head);
-    long long r = l - sb.start_h * per_head;
-    int mb = 0;
-    while (true) {
-      const int c = chunk_cost(p, s, mb);
-      if (r < c) break;
-      r -= c;
-      ++mb;
-    }
-    sb.start_mb = mb;
-    sb.start_j = (int)r;
-  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sb.tmem_base;
-  ChunkRun run;
-  run.left = max(0LL, steps);
-  if (steps > 0) {
-    run.b = sb.place.b;
-    run.h = sb.start_h;
-    run.mb = sb.start_mb;
-    run.j = sb.start_j;
-    run.seq = chunk_seq(p, run.b);
-  }
-
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::: "memory");
@@ -396,26 +449,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint32_t s_phase = 0;
     uint32_t step0 = 0;  // steps of the run before this segment
     uint32_t part = 0;   // segments this tile took part in
-    while (run.next(p)) {
-      const int n_t = t ? run.n1 : run.n0;
+#pragma unroll 1
+    for (uint32_t x = 0;; ++x) {
+      ChunkSeg sg;
+      if (!chunk_next(sb, x, lane == 0, abort_flag, sg)) {
+        chunk_abort(sb, p.err);
+        goto done;
+      }
+      if (sg.mb < 0) break;
+      const int n_t = t ? sg.n1 : sg.n0;
       if (n_t == 0) {
-        step0 += run.n;
+        step0 += sg.n;
         continue;
       }
-      const int first = run.smb * kChunkRows + t * 128;
-      const int r_end = run.sseq.rows * p.G;
+      const int first = sg.mb * kChunkRows + t * 128;
+      const int r_end = sg.rows * p.G;
+      const int k_base = sg.j0 * 128, step_end = step0 + sg.n;
       const float c =
-          chunk_queries<D>(p, run.sb, run.sh, first, r_end, warp & 3, lane, smem + t * C::kQTile);
+          chunk_queries<D>(p, sg.b, sg.h, first, r_end, warp & 3, lane, smem + t * C::kQTile);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sb.q_full[t]);
       const int r = first + row;
-      const int vis = r < r_end ? row_sees(p, r / p.G, run.sseq.len, run.sseq.rows) : 0;
+      const int vis = r < r_end ? row_sees(p, row_query(p, r), sg.len, sg.rows) : 0;
       // Warps whose 32 rows all lie past the last one keep the protocol only.
       const bool idle = first + (warp & 3) * 32 >= r_end;
       const int vis_min = __reduce_min_sync(0xffffffffu, r < r_end ? vis : 0x7fffffff);
       float m_run = -INFINITY, l_run = 0.f, lc_run = 0.f;
       int e_cur = 0;
+#pragma unroll 1
       for (int j = 0; j < n_t; ++j) {
         if (!mbar_wait(&sb.s_full[t], s_phase, abort_flag)) {
           chunk_abort(sb, p.err);
@@ -459,12 +521,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 128; ++i) reg_barrier(s[i]);
-        const int k0 = (run.j0 + j) * 128;
+        const int k0 = k_base + j * 128;
         if (k0 + 128 > vis_min || valid != 0xff) {
           const int lim = vis - k0;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= lim || !(valid >> (i >> 4) & 1)) s[i] = __float_as_uint(-INFINITY);
+          for (int q = 0; q < 8; ++q) {
+            const int lq = valid >> q & 1 ? lim - 16 * q : 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i >= lq) s[16 * q + i] = __float_as_uint(-INFINITY);
+          }
         }
         float m_cand = -INFINITY;
 #pragma unroll
@@ -556,7 +622,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       ++part;
-      step0 += run.n;
+      step0 = step_end;
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ value conversion + epilogue
@@ -570,12 +636,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint32_t step0 = 0, segs = 0;
     uint32_t part[2] = {0, 0};
     // the segment whose epilogue is pending
-    bool pend = false, pwhole = false;
+    bool pend = false;
+    int pwhole = 0;
     int pb = 0, ph = 0, pmb = 0, pn[2] = {0, 0}, pe[2] = {0, 0}, prows = 0, plen = 0, pseg = 0;
+#pragma unroll 1
     while (true) {
-      const bool have = run.next(p);
-      const int n = have ? run.n : 0;
+      ChunkSeg sg;
+      if (!chunk_next(sb, segs, lane == 0, abort_flag, sg)) {
+        chunk_abort(sb, p.err);
+        goto done;
+      }
+      const bool have = sg.mb >= 0;
+      const int n = have ? sg.n : 0;
       int e_run = 0, e_max = kKv8ExpMin, e_t0 = 0, e_t1 = 0;
+#pragma unroll 1
       for (int j = 0; j <= n; ++j) {
         if (pend && (j == 1 || !have)) {
           // every converter warp has seen the segment's value codes
@@ -601,12 +675,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const float m = sb.m_fin[pc & 1][t][row];
             const float l = sb.l_fin[pc & 1][t][row];
             float oscale = exp2i(-pe[t]) / (l + sb.lc_fin[pc & 1][t][row]);
-            if (l == 0.f) oscale = 0.f;  // no position seen
+            if (l == 0.f) oscale = 0.f;  // no position seen (O is 0)
             const float lse =
                 l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994531f;
             const int r = pmb * kChunkRows + t * 128 + row;
             const bool ok = r < prows * p.G;
-            const int i = ok ? r / p.G : 0;
+            const int i = ok ? row_query(p, r) : 0;
             const int see = ok ? row_sees(p, i, plen, prows) : 0;
             const uint32_t tO = tmem + lane_off + (t ? C::kColO1 : C::kColO0);
             const long long orow =
@@ -622,15 +696,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               for (int k = 0; k < 32; ++k) {
                 reg_barrier(o[k]);
                 o[k] = __float_as_uint(__uint_as_float(o[k]) * oscale);
-              }
-              if (l == 0.f) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = 0;
-              }
-              if (nan) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (sb.nan_pos[par][c0 + k] < see) o[k] = 0x7fc00000u;
               }
               if (ok && pwhole) {
                 uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + c0);
@@ -653,6 +718,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 p.lse[orow] = lse;
               else
                 part_row[D] = lse;
+              if (nan) {  // columns in which this row sees a NaN
+#pragma unroll 1
+                for (int k = 0; k < D; ++k)
+                  if (sb.nan_pos[par][k] < see) {
+                    if (pwhole)
+                      p.o[orow * D + k] = __ushort_as_bfloat16((unsigned short)0x7fc0u);
+                    else
+                      part_row[k] = __uint_as_float(0x7fc00000u);
+                  }
+              }
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -670,8 +745,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           chunk_abort(sb, p.err);
           goto done;
         }
-        const int valid = sb.k_valid[idx & 7];
-        const int k0 = (run.j0 + j) * 128;
+        const int v_valid = sb.v_valid[idx & 7];
+        const int k0 = (sg.j0 + j) * 128;
         {
           // (runs that could not be read carry the least exponent)
           int e8 = sb.v_exp8[idx & 7][lane & 7];
@@ -680,59 +755,67 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         e_run = kChunkLift - e_max;
         const uint8_t *raw = smem + C::kOffV + vs * C::kRaw;
         uint8_t *dst = smem + C::kOffV16 + ws * C::kV16;
-        const int par = segs & 7;
-        const bool edge = valid != 0xff || k0 + 128 > run.sseq.len;
-        uint32_t odd = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tr = cw * 32 + i * 8 + crow;  // row of the tile
+        // 16 codes of row tr, piece pc, to fp16 times 2^(ve - E + lift)
+        auto put = [&](int tr, int pc, const uint32_t(&x)[4]) {
           const float fs = exp2i(max(sb.v_exp8[idx & 7][tr >> 4] + e_run, -126));
           const uint32_t f2 = pack_f16x2(fs, fs);
+          uint32_t o[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            e4m3x4_to_f16x2x2(x[y], o[2 * y], o[2 * y + 1]);
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[2 * y]) : "r"(f2));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[2 * y + 1]) : "r"(f2));
+          }
+          uint8_t *line = dst + (pc >> 2) * 16384 + tr * 128;
+          *reinterpret_cast<uint4 *>(line + (((2 * (pc & 3)) ^ (tr & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(line + (((2 * (pc & 3) + 1) ^ (tr & 7)) << 4)) =
+              make_uint4(o[4], o[5], o[6], o[7]);
+        };
+        auto get = [&](int tr, int pc) {
+          if constexpr (D == 128)
+            return *reinterpret_cast<const uint4 *>(raw + tr * 128 + ((pc ^ (tr & 7)) << 4));
+          else
+            return *reinterpret_cast<const uint4 *>(raw + tr * 64 + ((pc ^ ((tr >> 1) & 3)) << 4));
+        };
+        uint32_t any = 0;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int hc = 0; hc < D / 64; ++hc) {
-            const int pc = hc * 4 + cpiece;
-            uint4 w;
-            if constexpr (D == 128)
-              w = *reinterpret_cast<const uint4 *>(raw + tr * 128 + ((pc ^ (tr & 7)) << 4));
-            else
-              w = *reinterpret_cast<const uint4 *>(raw + tr * 64 + ((pc ^ ((tr >> 1) & 3)) << 4));
-            uint32_t x[4] = {w.x, w.y, w.z, w.w};
-            if (edge && (!(valid >> (tr >> 4) & 1) || k0 + tr >= run.sseq.len)) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y) x[y] = 0;
-            }
-            uint32_t any = 0;
+            const int tr = cw * 32 + i * 8 + crow, pc = hc * 4 + cpiece;
+            const uint4 w = get(tr, pc);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) any |= (x[y] & 0x7f7f7f7fu) + 0x01010101u;
-            if (any & 0x80808080u) {  // rare: a NaN code
-              odd = 1;
-              for (int y = 0; y < 16; ++y) {
-                const uint32_t code = x[y >> 2] >> (8 * (y & 3)) & 0x7fu;
-                if (code == 0x7fu) {
-                  atomicMin(&sb.nan_pos[par][pc * 16 + y], k0 + tr);
-                }
-              }
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint32_t hit = ((x[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                x[y] &= ~((hit >> 7) * 0xffu);
-              }
-            }
-            uint32_t o[8];
+            put(tr, pc, x);
+          }
+        // Rows past the length or without a page, and NaN codes: this lane's
+        // pieces once more, with zeros in their place.
+        if (v_valid != 0xff || k0 + 128 > sg.len || (any & 0x80808080u)) {
+#pragma unroll 1
+          for (int z = 0; z < D / 16; ++z) {
+            const int tr = cw * 32 + (z / (D / 64)) * 8 + crow, pc = (z % (D / 64)) * 4 + cpiece;
+            const uint4 w = get(tr, pc);
+            uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            const bool off = !(v_valid >> (tr >> 4) & 1) || k0 + tr >= sg.len;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              e4m3x4_to_f16x2x2(x[y], o[2 * y], o[2 * y + 1]);
-              asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[2 * y]) : "r"(f2));
-              asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[2 * y + 1]) : "r"(f2));
+              uint32_t hit = ((x[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (off) hit = 0x80808080u;
+              x[y] &= ~((hit >> 7) * 0xffu);
+              if (!off && hit) {
+                sb.nan_any[segs & 7] = 1;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k)
+                  if (hit >> (8 * k + 7) & 1)
+                    atomicMin(&sb.nan_pos[segs & 7][pc * 16 + 4 * y + k], k0 + tr);
+              }
             }
-            uint8_t *line = dst + hc * 16384 + tr * 128;
-            *reinterpret_cast<uint4 *>(line + (((2 * cpiece) ^ (tr & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(line + (((2 * cpiece + 1) ^ (tr & 7)) << 4)) =
-                make_uint4(o[4], o[5], o[6], o[7]);
+            put(tr, pc, x);
           }
+          __syncwarp();
         }
-        if (odd) sb.nan_any[par] = 1;
         fence_proxy_async_smem();
         if (cw == 0 && lane == 0) sb.v_exp[ws] = e_run;
         __syncwarp();
@@ -740,23 +823,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           mbar_arrive(&sb.v_ready[ws]);
           mbar_arrive(&sb.v_empty[vs]);
         }
-        if (j == run.n0 - 1) e_t0 = e_run;
-        if (j == run.n1 - 1) e_t1 = e_run;
+        if (j == sg.n0 - 1) e_t0 = e_run;
+        if (j == sg.n1 - 1) e_t1 = e_run;
       }
       if (!have) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sb.conv_bar);
       pend = true;
-      pwhole = run.whole;
-      pb = run.sb;
-      ph = run.sh;
-      pmb = run.smb;
-      pn[0] = run.n0;
-      pn[1] = run.n1;
+      pwhole = sg.whole;
+      pb = sg.b;
+      ph = sg.h;
+      pmb = sg.mb;
+      pn[0] = sg.n0;
+      pn[1] = sg.n1;
       pe[0] = e_t0;
       pe[1] = e_t1;
-      prows = run.sseq.rows;
-      plen = run.sseq.len;
+      prows = sg.rows;
+      plen = sg.len;
       pseg = (int)segs;
       ++segs;
       step0 += n;
@@ -774,36 +857,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t q_lo0 = sdesc_sw128_lo(smem_addr(smem), 16);
       const uint32_t k_lo0 = sdesc_sw128_lo(smem_addr(smem + C::kOffK), 16);
       const uint32_t v_lo0 = sdesc_sw128_lo(smem_addr(smem + C::kOffV16), 16384);
-      uint32_t p_phase[2] = {0, 0};
-      uint32_t part[2] = {0, 0};
-      uint32_t step0 = 0;
-      while (run.next(p)) {
-        const int n = run.n;
+      // One body for both tiles (the other roles take most of the instruction
+      // fetch), its products unrolled: a rolled issue loop took 95 cycles a
+      // product, where the tensor core takes 64.
+      uint32_t p_phase = 0;            // bit t
+      uint32_t parts = 0, started = 0; // bit t: parity of segments done, any done
+      uint32_t ks = 0, k_turn = 0;     // key ring slot of step j, parity of its use
+      uint32_t ws = 0;                 // fp16 value slot of step j - 1
+#pragma unroll 1
+      for (uint32_t sx = 0;; ++sx) {
+        ChunkSeg sg;
+        if (!chunk_next(sb, sx, true, abort_flag, sg)) {
+          chunk_abort(sb, p.err);
+          goto mma_exit;
+        }
+        if (sg.mb < 0) break;
+        const int n = sg.n, n0 = sg.n0, n1 = sg.n1;
 #pragma unroll 1
         for (int j = 0; j <= n; ++j) {
-          const uint32_t kidx = step0 + j, vidx = kidx - 1;
-          const uint32_t ks = kidx % C::kKs, ws = vidx % C::kV16s;
           bool k_ready = false;
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t) {
-            const int n_t = t ? run.n1 : run.n0;
+            const int n_t = t ? n1 : n0;
             const bool do_pv = j >= 1 && j <= n_t;
             const bool do_s = j < n_t;
-            const uint32_t tS = tmem + (t ? C::kColS1 : C::kColS0);
-            const uint32_t tO = tmem + (t ? C::kColO1 : C::kColO0);
+            const uint32_t tS = tmem + t * (C::kColS1 - C::kColS0);
+            const uint32_t tO = tmem + C::kColO0 + t * (C::kColO1 - C::kColO0);
             if (do_pv) {
               // (P is signalled only once V_{j-1} is converted)
-              if ((j == 1 && part[t] > 0 &&
-                   !mbar_wait(&sb.o_free[t], (part[t] - 1) & 1, abort_flag)) ||
-                  !mbar_wait(&sb.p_full[t], p_phase[t], abort_flag)) {
+              if ((j == 1 && (started >> t & 1) &&
+                   !mbar_wait(&sb.o_free[t], ~(parts >> t) & 1, abort_flag)) ||
+                  !mbar_wait(&sb.p_full[t], p_phase >> t & 1, abort_flag)) {
                 chunk_abort(sb, p.err);
                 goto mma_exit;
               }
-              p_phase[t] ^= 1;
+              p_phase ^= 1u << t;
             }
             if (do_s) {
-              if ((j == 0 && !mbar_wait(&sb.q_full[t], part[t] & 1, abort_flag)) ||
-                  (!k_ready && !mbar_wait(&sb.k_full[ks], (kidx / C::kKs) & 1, abort_flag))) {
+              if ((j == 0 && !mbar_wait(&sb.q_full[t], parts >> t & 1, abort_flag)) ||
+                  (!k_ready && !mbar_wait(&sb.k_full[ks], k_turn, abort_flag))) {
                 chunk_abort(sb, p.err);
                 goto mma_exit;
               }
@@ -818,8 +910,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 umma_ts_w<1>(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), hi128, idO);
             }
             if (do_s) {
-              const uint32_t a = q_lo0 + t * (C::kQTile >> 4), bk = k_lo0 + ks * (C::kRaw >> 4);
               // 32 codes a product; hi, then lo
+              const uint32_t a = q_lo0 + t * (C::kQTile >> 4), bk = k_lo0 + ks * (C::kRaw >> 4);
               umma_f8_ss<0>(tS, a, hi128, bk, hik, idS);
 #pragma unroll
               for (int kk = 1; kk < D / 16; ++kk) {
@@ -832,13 +924,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             if (do_pv && j == n_t) {
               umma_commit(&sb.o_full[t]);
-              ++part[t];
+              parts ^= 1u << t;
+              started |= 1u << t;
             }
           }
-          if (j < n) umma_commit(&sb.k_empty[ks]);
-          if (j >= 1) umma_commit(&sb.v_free[ws]);
+          if (j < n) {
+            umma_commit(&sb.k_empty[ks]);
+            if (++ks == C::kKs) {
+              ks = 0;
+              k_turn ^= 1;
+            }
+          }
+          if (j >= 1) {
+            umma_commit(&sb.v_free[ws]);
+            ws ^= 1;
+          }
         }
-        step0 += n;
       }
     mma_exit:
       // every product must finish before the tensor memory is freed
@@ -848,96 +949,71 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_wait(&sb.mma_done, 0, &never);
       }
     }
-    if (warp == 14) {
-      // ---------------------------------------------------------- TMA, a lane a page
-      uint32_t idx = 0;  // steps loaded
-      const int pages = 128 >> p.page_log2;  // of a tile
-      bool gone = false;
-      while (!gone && run.next(p)) {
-        const int len = run.sseq.len;
-        // this lane's page of tile x: its index, or -1
-        auto fetch = [&](int x) -> int {
-          const int t = x * 128 + (lane << p.page_log2);
-          if (lane >= pages || t >= len) return -1;
-          const int id = p.table[kv8_table_offset(g, run.sb, t >> p.page_log2)];
-          if (kv8_page_ok(g, id)) return id;
-          atomicCAS(p.err, 0, kDevErrIndex);
-          return -1;
-        };
-        int id = fetch(run.j0);
-        int id_next = run.n > 1 ? fetch(run.j0 + 1) : -1;
-        int ke = id >= 0 ? p.ke[id * g.Hkv + run.sh] : 0;
-        int ve = id >= 0 ? p.ve[id * g.Hkv + run.sh] : kKv8ExpMin;
-        for (int j = 0; j < run.n; ++j, ++idx) {
-          const uint32_t ks = idx % C::kKs, vs = idx % C::kVs;
-          // the next tile's exponents, and the one after's pages
-          const int ke1 = id_next >= 0 ? p.ke[id_next * g.Hkv + run.sh] : 0;
-          const int ve1 = id_next >= 0 ? p.ve[id_next * g.Hkv + run.sh] : kKv8ExpMin;
-          const int id2 = j + 2 < run.n ? fetch(run.j0 + j + 2) : -1;
-          int ok = 1;
-          if (lane == 0 && idx >= (uint32_t)C::kKs)
-            ok = mbar_wait(&sb.k_empty[ks], (idx / C::kKs - 1) & 1, abort_flag);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
-            if (lane == 0) chunk_abort(sb, p.err);
-            gone = true;
-            break;
-          }
-          const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-          const uint32_t bytes = __popc(have) * g.page * D;
-          // eight runs of 16 positions, whatever the page
-          {
-            const int src = (lane & 7) >> (p.page_log2 - 4);
-            const int kr = __shfl_sync(0xffffffffu, ke, src), vr = __shfl_sync(0xffffffffu, ve, src);
-            if (lane < 8) {
-              sb.k_scale[idx & 7][lane] = exp2i(max(kr, -126));
-              sb.v_exp8[idx & 7][lane] = vr;
-            }
-            const uint32_t bits = __ballot_sync(0xffffffffu, lane < 8 && (have >> src & 1));
-            if (lane == 0) sb.k_valid[idx & 7] = (int)bits;
-          }
-          __syncwarp();
-          const int y = (id * g.Hkv + run.sh) << p.page_log2;
-          if (lane == 0) mbar_arrive_expect_tx(&sb.k_full[ks], bytes);
-          __syncwarp();
-          if (id >= 0)
-            tma_load_2d(smem + C::kOffK + ks * C::kRaw + (lane << p.page_log2) * D, &tm_k,
-                        &sb.k_full[ks], 0, y);
-          if (lane == 0 && idx >= (uint32_t)C::kVs)
-            ok = mbar_wait(&sb.v_empty[vs], (idx / C::kVs - 1) & 1, abort_flag);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
-            if (lane == 0) chunk_abort(sb, p.err);
-            gone = true;
-            // the key tile of this step is in flight: wait for it below
-            int never = 0;
-            if (lane == 0) mbar_wait(&sb.k_full[ks], (idx / C::kKs) & 1, &never);
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&sb.v_full[vs], bytes);
-          __syncwarp();
-          if (id >= 0)
-            tma_load_2d(smem + C::kOffV + vs * C::kRaw + (lane << p.page_log2) * D, &tm_v,
-                        &sb.v_full[vs], 0, y);
-          id = id_next;
-          ke = ke1;
-          ve = ve1;
-          id_next = id2;
-        }
+    if (warp == 15 && lane == 0) {
+      // ---------------------------------------------------------- the run's segments
+      const long long share = sb.place.share;
+      const long long u0 = blockIdx.x * share;
+      long long left = max(0LL, min(share, sb.place.total - u0));
+      int b = sb.place.b, h = 0, mb = 0, j = 0;
+      ChunkSeq q = {0, 0, 0};
+      if (left > 0) {
+        q = chunk_seq(p, b);
+        long long r = u0 - sb.place.prefix;
+        const long long per_head = chunk_seq_cost(p, b);
+        h = (int)(r / per_head);
+        r -= h * per_head;
+#pragma unroll 1
+        for (int c; r >= (c = chunk_cost(p, q, mb)); ++mb) r -= c;
+        j = (int)r;
       }
-      // wait for the copies still in flight (all consumed on the normal path)
-      if (lane == 0) {
-        int never = 0;
-        for (uint32_t s = 0; s < (uint32_t)C::kKs && s < idx; ++s) {
-          const uint32_t last = idx - 1 - ((idx - 1 - s) % C::kKs);
-          mbar_wait(&sb.k_full[s], (last / C::kKs) & 1, &never);
+#pragma unroll 1
+      for (uint32_t x = 0;; ++x) {
+        if (x >= 4 && !mbar_wait(&sb.seg_empty[x & 3], ((x >> 2) - 1) & 1, abort_flag)) {
+          chunk_abort(sb, p.err);
+          break;
         }
-        for (uint32_t s = 0; s < (uint32_t)C::kVs && s < idx; ++s) {
-          const uint32_t last = idx - 1 - ((idx - 1 - s) % C::kVs);
-          mbar_wait(&sb.v_full[s], (last / C::kVs) & 1, &never);
+        ChunkSeg &sg = sb.seg[x & 3];
+        if (left == 0) {
+          sg.mb = -1;
+          mbar_arrive(&sb.seg_full[x & 3]);
+          break;
+        }
+        const int t0 = chunk_tiles(p, mb * kChunkRows, q.len, q.rows);
+        const int t1 = chunk_tiles(p, mb * kChunkRows + 128, q.len, q.rows);
+        const int cost = max(t0, t1);
+        const int n = (int)min((long long)(cost - j), left);
+        sg.b = b;
+        sg.h = h;
+        sg.mb = mb;
+        sg.j0 = j;
+        sg.n = n;
+        sg.n0 = min(max(t0 - j, 0), n);
+        sg.n1 = min(max(t1 - j, 0), n);
+        sg.len = q.len;
+        sg.rows = q.rows;
+        sg.whole = j == 0 && n == cost;
+        mbar_arrive(&sb.seg_full[x & 3]);
+        left -= n;
+        j += n;
+        if (j == cost) {
+          j = 0;
+          if (++mb == q.units) {
+            mb = 0;
+            if (++h == g.Hkv) {
+              h = 0;
+#pragma unroll 1
+              while (++b < p.B) {
+                q = chunk_seq(p, b);
+                if (q.units > 0) break;
+              }
+            }
+          }
         }
       }
     }
+    if (warp == 13 || warp == 14)
+      chunk_load<D>(p, warp == 13, warp == 13 ? &tm_v : &tm_k, sb,
+                    smem + (warp == 13 ? C::kOffV : C::kOffK), lane, abort_flag);
   }
 done:
   tc_fence_before_sync();
@@ -961,6 +1037,7 @@ __global__ void __launch_bounds__(256)
   const int mb = r / kChunkRows;
   // steps of the head's units before this row's, and of all of them
   long long before = 0, all = 0;
+#pragma unroll 1
   for (int x = lane; x < s.units; x += 32) {
     const int c = chunk_cost(p, s, x);
     all += c;
@@ -973,7 +1050,7 @@ __global__ void __launch_bounds__(256)
   }
   grid_wait();  // every block waits: this launch's end means the end of the one before too
   if (r >= s.rows * p.G) return;
-  const long long share = max(1LL, (p.prefix[p.B] + p.ctas - 1) / p.ctas);
+  const long long share = p.prefix[p.B];
   const long long s0 = p.prefix[b] + h * all + before;
   const int cost = chunk_cost(p, s, mb);
   const int c0 = (int)(s0 / share), c1 = (int)((s0 + cost - 1) / share);
@@ -1001,7 +1078,7 @@ __global__ void __launch_bounds__(256)
     for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, d[lane * kPer + i], acc[i]);
   }
   const float inv = z == 0.f ? 0.f : 1.f / z;
-  const int i = r / p.G;
+  const int i = row_query(p, r);
   const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
   uint32_t pk[kPer / 2];
 #pragma unroll

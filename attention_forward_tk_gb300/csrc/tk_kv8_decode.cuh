@@ -68,13 +68,14 @@ struct Kv8AttnParams {
   __nv_bfloat16 *o;
   float *lse;
   int B, H, G, Nq;  // G = H / Hkv
+  unsigned g_mul;   // floor(2^32 / G) + 1, or 0 for G = 1
   int causal;
   float scale_log2;  // scale * log2(e)
   int tile_rows;     // (few rows) 8 or 16, at least Nq * G
   int ctas;          // runs the work is cut into
   int *err;
   float *part;       // [ctas, 2, rows of a tile or unit, D + 4]
-  long long *prefix;  // (many rows) the work before each sequence, the total last
+  long long *prefix;  // (many rows) the work before each sequence, a run's share last
 };
 
 constexpr int kDecWarps = 4;
@@ -117,6 +118,11 @@ __device__ __forceinline__ int seq_units(const Kv8AttnParams &p, int b, int unit
   return rows == 0 ? 0 : max(1, (seq_len(p, b, &bad) + unit - 1) / unit);
 }
 
+// Query of row r = i * G + g (the host bounds Nq * G * G below 2^31, which makes
+// the multiplication exact).
+__device__ __forceinline__ int row_query(const Kv8AttnParams &p, int r) {
+  return p.g_mul ? (int)__umulhi((unsigned)r, p.g_mul) : r;
+}
 // Positions row i of a sequence sees.
 __device__ __forceinline__ int row_sees(const Kv8AttnParams &p, int i, int len, int rows) {
   return p.causal ? max(0, len - (rows - 1 - i)) : len;
@@ -124,6 +130,7 @@ __device__ __forceinline__ int row_sees(const Kv8AttnParams &p, int i, int len, 
 
 struct Kv8Place {
   long long total;   // units of the call
+  long long share;   // units of a run
   long long prefix;  // units before sequence b
   int b;
 };
@@ -131,13 +138,14 @@ struct Kv8Place {
 // Total work (cost(b) over the sequences), and the sequence in which run `run`
 // starts (b = B when past the end), or with find_b >= 0 the work before
 // sequence find_b.  With `prefix` the work before each sequence is written
-// there, the total last.  Whole block; ends with a barrier.
+// there, a run's share last.  Whole block; ends with a barrier.
 template <typename Cost>
 __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, Cost cost, int run, int find_b,
                                          Kv8Place *out, long long *red, long long *prefix) {
   const int nthr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long v0 = (int)threadIdx.x < p.B ? cost(threadIdx.x) : 0;
   long long sum = v0;
+#pragma unroll 1
   for (int b = threadIdx.x + nthr; b < p.B; b += nthr) sum += cost(b);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -145,14 +153,18 @@ __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, Cost cost, int 
   if (threadIdx.x == 0) out->b = p.B;
   __syncthreads();
   long long total = 0;
+#pragma unroll 1
   for (int w = 0; w < nthr / 32; ++w) total += red[w];
   if (threadIdx.x == 0) {
+    const long long share = max(1LL, (total + p.ctas - 1) / p.ctas);
     out->total = total;
-    if (prefix) prefix[p.B] = total;
+    out->share = share;
+    if (prefix) prefix[p.B] = share;
   }
-  const long long u = run * max(1LL, (total + p.ctas - 1) / p.ctas);
   __syncthreads();
+  const long long u = run * out->share;
   long long carry = 0;
+#pragma unroll 1
   for (int base = 0; base < p.B; base += nthr) {
     const int b = base + threadIdx.x;
     const long long v = base == 0 ? v0 : b < p.B ? cost(b) : 0;
@@ -165,8 +177,12 @@ __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, Cost cost, int 
     if (lane == 31) red[warp] = inc;
     __syncthreads();
     long long before = carry;
-    for (int w = 0; w < warp; ++w) before += red[w];
-    for (int w = 0; w < nthr / 32; ++w) carry += red[w];
+#pragma unroll 1
+    for (int w = 0; w < nthr / 32; ++w) {
+      const long long x = red[w];
+      before += w < warp ? x : 0;
+      carry += x;
+    }
     const long long lo = before + inc - v;
     if (b < p.B) {
       if (prefix) prefix[b] = lo;
@@ -269,6 +285,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   grid_launch_dependents();
   if (blockIdx.x == 0) {  // report what is out of range, once
     bool bad = false;
+#pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kDecThreads) {
       seq_len(p, b, &bad);
       seq_rows(p, b, &bad);
@@ -278,7 +295,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   kv8_scan(
       p, [&](int b) { return (long long)seq_units(p, b, kDecUnit) * segs; }, blockIdx.x, -1,
       &place, red, nullptr);
-  const long long share = max(1LL, (place.total + p.ctas - 1) / p.ctas);
+  const long long share = place.share;
   const long long u0 = blockIdx.x * share;
   if (u0 >= place.total) return;
   const int nsteps = (int)min(share, place.total - u0);
@@ -378,7 +395,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     for (int t = 0; t < kNT; ++t) {
       const int r = 8 * t + q8;
       const bool on = r < r_end;
-      const int i = r / p.G;
+      const int i = row_query(p, r);
       const __nv_bfloat16 *src =
           p.q + (((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i) * D + c4 * kChunks * 16;
       uint2 w[kSteps];
@@ -405,7 +422,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int rx = 8 * t + 2 * c4 + x;
-        vis[t][x] = rx < r_end ? row_sees(p, rx / p.G, len, rows) : 0;
+        vis[t][x] = rx < r_end ? row_sees(p, row_query(p, rx), len, rows) : 0;
         vis_min = min(vis_min, rx < r_end ? vis[t][x] : len);
         f[t][x] = __shfl_sync(0xffffffffu, fr, (2 * c4 + x) * 4);
       }
@@ -422,6 +439,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       l[t][0] = l[t][1] = 0.f;
     }
 
+#pragma unroll 1
     for (int n = 0; n < n_here; ++n, ++step) {
       // issue the step kStages - 1 ahead, then wait for this one's copies
       const bool none = eo_now < 0;
@@ -566,6 +584,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
         }
         if (__any_sync(0xffffffffu, odd)) {
           // query by query, without the positions that one does not see
+#pragma unroll 1
           for (int i = 0; i < rows; ++i) {
             const int see = row_sees(p, i, len, rows);
             uint32_t z[4][kVw];
@@ -577,7 +596,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
 #pragma unroll
             for (int t = 0; t < kNT; ++t) {
               const int ra = 8 * t + 2 * c4;
-              const bool on0 = ra / p.G == i, on1 = (ra + 1) / p.G == i;
+              const bool on0 = row_query(p, ra) == i, on1 = row_query(p, ra + 1) == i;
 #pragma unroll
               for (int j = 0; j < kSteps; ++j) {
                 const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
@@ -668,7 +687,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
           }
         }
         if (whole) {
-          const int i = r / p.G;
+          const int i = row_query(p, r);
           const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
           // 2^(M - lift - m) / l, in two factors (M - m is a value exponent)
           const float half = ll == 0.f ? 0.f : ex2_approx(0.5f * (mmo - kDecLift - mm));
@@ -715,7 +734,7 @@ __global__ void __launch_bounds__(D)
       p, [&](int b) { return (long long)seq_units(p, b, kDecUnit) * segs; }, 0, b, &place, red,
       nullptr);
   const int units = seq_units(p, b, kDecUnit);
-  const long long share = max(1LL, (place.total + p.ctas - 1) / p.ctas);
+  const long long share = place.share;
   const long long s0 = place.prefix + (long long)h * units;
   const int c0 = (int)(s0 / share), c1 = (int)((s0 + max(units, 1) - 1) / share);
   // All above reads only what the launch before leaves alone.  Every block
@@ -741,7 +760,7 @@ __global__ void __launch_bounds__(D)
     ll += l == 0.f ? 0.f : l * ex2_approx(d[D] - mm);
     out = fmaf(l == 0.f ? 0.f : ex2_approx(d[D + 1] - mmo), d[threadIdx.x], out);
   }
-  const int i = r / p.G;
+  const int i = row_query(p, r);
   const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
   const float half = ll == 0.f ? 0.f : ex2_approx(0.5f * (mmo - kDecLift - mm));
   const float inv = ll == 0.f ? 0.f : half / ll;
