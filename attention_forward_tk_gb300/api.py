@@ -83,6 +83,8 @@ _lib = None
 def library() -> ctypes.CDLL:
     """Load libtk_attn.so once and declare the C signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -143,7 +145,7 @@ def library() -> ctypes.CDLL:
         lib.tk_gemm_bf16.argtypes = [vp, vp, vp, i, i, i, vp]
         lib.tk_gemm_bf16_check_args.restype = i
         lib.tk_gemm_bf16_check_args.argtypes = [vp, vp, vp, i, i, i]
-        sz, ll3 = ctypes.c_size_t, ctypes.POINTER(ctypes.c_longlong)
+        sz, ll3 = ctypes.c_size_t, vp
         norm_in = [vp, ll3, vp, ll3, vp, vp, i, vp, vp]
         dims = [i, i, i, i, i, i, i, f]  # B, H, Hk, N, D, rot, interleaved, eps
         lib.tk_attn_qk_norm_rope.restype = i
@@ -305,9 +307,12 @@ def tk_gemm_bf16_check_args(a: int, b: int, c: int, M: int, N: int, K: int) -> i
     return int(library().tk_gemm_bf16_check_args(a, b, c, M, N, K))
 
 
+_LL3, _LL4 = ctypes.c_longlong * 3, ctypes.c_longlong * 4
+
+
 def _ll3(strides):
     """Element strides of batch, head and token as the C calls take them."""
-    return (ctypes.c_longlong * 3)(*strides)
+    return _LL3(*strides)
 
 
 def tk_attn_qk_norm_rope(q: int, q_strides, k: int, k_strides, q_weight: int, k_weight: int,
@@ -675,22 +680,24 @@ def attention_forward_host(q, k, v, causal: bool = False, scale: float | None = 
 
 
 # ----------------------------------------------------------------- a decoder's serving steps
+#
+# These are called for every layer of every token, and at one token a sequence
+# the device needs a few microseconds: the helpers below read each tensor
+# attribute once and build nothing that a check does not need.
 
 
-def _launch(t, stream, call):
-    """call(stream handle) with the tensor t's device current, and with `stream`
-    (default: torch's current stream there) current too, so that what torch
-    allocates inside belongs to the stream that uses it."""
+def _stream_on(dev, stream, call):
+    """call(stream handle) for tensors on CUDA device `dev`, with that device and
+    `stream` (a torch stream or a handle) current, so that what torch allocates
+    inside belongs to the stream that uses it.  stream None: torch's current
+    stream of that device."""
     import torch
-    dev = t.device.index
-    if stream is None and torch.cuda.current_device() == dev:
-        return call(torch.cuda.current_stream().cuda_stream)
     with torch.cuda.device(dev):
         if stream is None:
             return call(torch.cuda.current_stream().cuda_stream)
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
-        if stream.device != t.device:
+            stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", dev))
+        if stream.device.index != dev:
             raise ValueError("the stream is on another device than the tensors")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
@@ -700,27 +707,26 @@ def _raise_status(name: str, status: int):
     raise TkAttnError(f"{name}: {tk_attn_status_string(status)} ({status})", status)
 
 
-def _want(t, name, dtype, shape, device):
-    """t is a contiguous tensor of this type and shape on this device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or \
-            t.device != device:
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on "
-                         f"{device}, not {str(t.dtype)[6:]} {list(t.shape)} on {t.device}")
+def _refuse(t, name, want):
+    raise ValueError(f"{name} must be {want}, not {str(t.dtype)[6:]} {list(t.shape)} with strides "
+                     f"{list(t.stride())} on {t.device}")
 
 
-def _want_rows(t, name, shape, device):
-    """t is a bf16 [B, H, N, D] tensor whose last dimension is contiguous."""
+def _want(t, name, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on CUDA device dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, name, f"a contiguous {str(dtype)[6:]} tensor {list(shape)} on cuda:{dev}")
+
+
+def _want_rows(t, name, shape, dev):
+    """t is a bf16 tensor of this shape whose last dimension is contiguous; its
+    strides as the C calls take them."""
     import torch
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.stride(3) != 1 or \
-            t.device != device:
-        raise ValueError(f"{name} must be a bfloat16 tensor {list(shape)} with a contiguous last "
-                         f"dimension on {device}, not {str(t.dtype)[6:]} {list(t.shape)} with "
-                         f"strides {list(t.stride())} on {t.device}")
-
-
-def _strides(t):
-    """Element strides of batch, head and token (a dimension of one has none)."""
-    return [s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride())]
+    st = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or st[3] != 1 or t.get_device() != dev:
+        _refuse(t, name, f"a bfloat16 tensor {list(shape)} with a contiguous last dimension on "
+                         f"cuda:{dev}")
+    return _LL4(*st)
 
 
 def rope_turns(rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
@@ -747,31 +753,32 @@ def rope_turns(rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, turns, positions):
+    """(device, the C call's input arguments, (B, H, Hk, N, D, rot))."""
     import torch
-    if q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0] or q.shape[2:] != k.shape[2:]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[2:] != ks[2:]:
         raise ValueError("q must be [B, H, N, D] and k [B, Hk, N, D]")
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("q must be a CUDA tensor")
-    dev = q.device
-    B, H, N, D = q.shape
-    Hk = k.shape[1]
-    _want_rows(q, "q", q.shape, dev)
-    _want_rows(k, "k", k.shape, dev)
+    B, H, N, D = qs
+    qst, kst = _want_rows(q, "q", qs, dev), _want_rows(k, "k", ks, dev)
     wt = q_weight.dtype
-    if wt != torch.bfloat16 and wt != torch.float32:
+    f32 = wt is torch.float32
+    if not f32 and wt is not torch.bfloat16:
         raise ValueError("q_weight and k_weight must be bfloat16 or float32")
     _want(q_weight, "q_weight", wt, (D,), dev)
     _want(k_weight, "k_weight", wt, (D,), dev)
-    rot = 0
+    rot = tp = pp = 0
     if turns is not None:
-        _want(turns, "turns", torch.int64, (turns.numel(),), dev)
         rot = 2 * turns.numel()
+        _want(turns, "turns", torch.int64, (rot // 2,), dev)
+        tp = turns.data_ptr()
     if positions is not None:
         _want(positions, "positions", torch.int32, (B, N), dev)
-    return (q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), q_weight.data_ptr(),
-            k_weight.data_ptr(), int(wt == torch.float32),
-            turns.data_ptr() if rot else 0, positions.data_ptr() if positions is not None else 0,
-            ), (B, H, Hk, N, D, rot)
+        pp = positions.data_ptr()
+    return dev, (q.data_ptr(), qst, k.data_ptr(), kst, q_weight.data_ptr(), k_weight.data_ptr(),
+                 f32, tp, pp), (B, H, ks[1], N, D, rot)
 
 
 def qk_norm_rope_forward(q, k, q_weight, k_weight, turns, positions=None, eps: float = 1e-6,
@@ -786,22 +793,29 @@ def qk_norm_rope_forward(q, k, q_weight, k_weight, turns, positions=None, eps: f
     neighbours rather than halves.  Enqueued on `stream`; returns immediately.
     """
     import torch
-    ins, (B, H, Hk, N, D, rot) = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
-    if out_q is not None:
-        _want(out_q, "out_q", torch.bfloat16, (B, H, N, D), q.device)
-    if out_k is not None:
-        _want(out_k, "out_k", torch.bfloat16, (B, Hk, N, D), q.device)
+    dev, ins, dims = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _stream_on(dev, stream, lambda s: _norm_rope_run(q, k, dev, ins, dims, eps,
+                                                                interleaved, out_q, out_k, s))
+    return _norm_rope_run(q, k, dev, ins, dims, eps, interleaved, out_q, out_k,
+                          torch._C._cuda_getCurrentRawStream(dev))
 
-    def call(s):
-        oq = q.new_empty((B, H, N, D)) if out_q is None else out_q
-        ok = q.new_empty((B, Hk, N, D)) if out_k is None else out_k
-        st = tk_attn_qk_norm_rope(*ins, oq.data_ptr(), ok.data_ptr(), B, H, Hk, N, D, rot,
-                                  int(bool(interleaved)), eps, s)
-        if st != TK_ATTN_OK:
-            _raise_status("tk_attn_qk_norm_rope", st)
-        return oq, ok
 
-    return _launch(q, stream, call)
+def _norm_rope_run(q, k, dev, ins, dims, eps, interleaved, out_q, out_k, s):
+    import torch
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out_q, "out_q", torch.bfloat16, q.shape, dev)
+    if out_k is None:
+        out_k = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out_k, "out_k", torch.bfloat16, k.shape, dev)
+    st = library().tk_attn_qk_norm_rope(*ins, out_q.data_ptr(), out_k.data_ptr(), *dims,
+                                        1 if interleaved else 0, eps, s)
+    if st:
+        _raise_status("tk_attn_qk_norm_rope", st)
+    return out_q, out_k
 
 
 def qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out, dk_out, positions=None,
@@ -813,15 +827,14 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out, dk_out, posit
     Equal calls give equal bits.  Enqueued on `stream`; returns immediately.
     """
     import torch
-    ins, (B, H, Hk, N, D, rot) = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
-    for t, name, like in ((dq_out, "dq_out", q), (dk_out, "dk_out", k), (dq, "dq", q),
-                          (dk, "dk", k)):
-        if t is not None:
-            _want_rows(t, name, like.shape, q.device)
-    if workspace is not None and workspace.device != q.device:
+    dev, ins, dims = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
+    gos = (dq_out.data_ptr(), _want_rows(dq_out, "dq_out", q.shape, dev), dk_out.data_ptr(),
+           _want_rows(dk_out, "dk_out", k.shape, dev))
+    if workspace is not None and workspace.get_device() != dev:
         raise ValueError("the workspace must be on the tensors' device")
 
     def call(s):
+        D = dims[4]
         gq = torch.empty_like(q) if dq is None else dq
         gk = torch.empty_like(k) if dk is None else dk
         gw = torch.empty((2, D), dtype=torch.float32, device=q.device)
@@ -829,16 +842,18 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out, dk_out, posit
         if ws is None:
             ws = torch.empty(tk_attn_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
                              device=q.device)
-        st = tk_attn_qk_norm_rope_bwd(
-            *ins, dq_out.data_ptr(), _strides(dq_out), dk_out.data_ptr(),
-            _strides(dk_out), gq.data_ptr(), _strides(gq), gk.data_ptr(), _strides(gk),
-            gw.data_ptr(), gw.data_ptr() + 4 * D, B, H, Hk, N, D, rot, int(bool(interleaved)), eps,
-            ws.data_ptr(), ws.numel() * ws.element_size(), s)
-        if st != TK_ATTN_OK:
+        gp = gw.data_ptr()
+        st = library().tk_attn_qk_norm_rope_bwd(
+            *ins, *gos, gq.data_ptr(), _want_rows(gq, "dq", q.shape, dev), gk.data_ptr(),
+            _want_rows(gk, "dk", k.shape, dev), gp, gp + 4 * D, *dims, 1 if interleaved else 0,
+            eps, ws.data_ptr(), ws.numel() * ws.element_size(), s)
+        if st:
             _raise_status("tk_attn_qk_norm_rope_bwd", st)
         return gq, gk, gw[0], gw[1]
 
-    return _launch(q, stream, call)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _stream_on(dev, stream, call)
+    return call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 _norm_rope_fn = None
@@ -849,6 +864,10 @@ def _norm_rope_function():
     global _norm_rope_fn
     if _norm_rope_fn is None:
         import torch
+
+        def rows(t):  # as the C call reads gradients
+            return t if t.stride(3) == 1 and not any(x % 8 for x in t.stride()[:3]) \
+                else t.contiguous()
 
         class _NormRope(torch.autograd.Function):
             @staticmethod
@@ -862,11 +881,9 @@ def _norm_rope_function():
             @torch.autograd.function.once_differentiable
             def backward(ctx, dq_out, dk_out):
                 q, k, q_weight, k_weight, turns, positions = ctx.saved_tensors
-                dq_out, dk_out = (t if t.stride(3) == 1 and all(x % 8 == 0 for x in _strides(t))
-                                  else t.contiguous() for t in (dq_out, dk_out))
-                dq, dk, dqw, dkw = qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out,
-                                                         dk_out, positions, ctx.eps,
-                                                         ctx.interleaved)
+                dq, dk, dqw, dkw = qk_norm_rope_backward(
+                    q, k, q_weight, k_weight, turns, rows(dq_out), rows(dk_out), positions,
+                    ctx.eps, ctx.interleaved)
                 return (dq, dk, dqw.to(q_weight.dtype), dkw.to(k_weight.dtype), None, None, None,
                         None)
 
@@ -903,25 +920,25 @@ def kv8_cache(num_pages: int, heads: int, page: int, head_dim: int, device="cuda
 
 
 def _kv8_args(cache, page_table, B):
-    """Checked pointers and sizes of a cache and its page tables."""
+    """(device, the C calls' pointers, (num_pages, Hkv, page, D), (max_pages,
+    table stride)) of a cache and its page tables."""
     import torch
     k, v, ke, ve = cache
-    if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or not k.is_cuda or not k.is_contiguous():
-        raise ValueError("the cache's k must be a contiguous float8_e4m3fn CUDA tensor "
-                         "[num_pages, heads, page, D]")
-    dev, shape = k.device, k.shape
-    _want(v, "the cache's v", torch.float8_e4m3fn, shape, dev)
-    _want(ke, "the cache's k_exp", torch.int8, shape[:2], dev)
-    _want(ve, "the cache's v_exp", torch.int8, shape[:2], dev)
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or \
-            page_table.stride(1) != 1 or page_table.device != dev:
-        raise ValueError(f"page_table must be an int32 tensor [{B}, pages] with contiguous rows "
-                         f"on {dev}")
-    P, H, page, D = shape
-    # one sequence's table has no row stride of its own
-    stride = max(page_table.stride(0), page_table.shape[1])
-    return (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr(), page_table.data_ptr()), \
-        (P, H, page, D, page_table.shape[1], stride), dev
+    shape, f8, i8 = k.shape, torch.float8_e4m3fn, torch.int8
+    dev = k.get_device()
+    if len(shape) != 4 or k.dtype is not f8 or dev < 0 or not k.is_contiguous():
+        _refuse(k, "the cache's k", "a contiguous float8_e4m3fn CUDA tensor [pages, heads, page, D]")
+    _want(v, "the cache's v", f8, shape, dev)
+    _want(ke, "the cache's k_exp", i8, shape[:2], dev)
+    _want(ve, "the cache's v_exp", i8, shape[:2], dev)
+    ts, st = page_table.shape, page_table.stride()
+    if page_table.dtype is not torch.int32 or len(ts) != 2 or ts[0] != B or \
+            (st[1] != 1 and ts[1] != 1) or page_table.get_device() != dev:
+        _refuse(page_table, "page_table", f"an int32 tensor [{B}, pages] with contiguous rows on "
+                                          f"cuda:{dev}")
+    # (one sequence's table has no row stride of its own)
+    return dev, (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr(),
+                 page_table.data_ptr()), shape, (ts[1], st[0] if B > 1 else ts[1])
 
 
 def kv8_write(cache: Kv8Cache, k, v, page_table, start, counts=None, stream=None) -> None:
@@ -933,22 +950,25 @@ def kv8_write(cache: Kv8Cache, k, v, page_table, start, counts=None, stream=None
     import torch
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, D]")
-    B, Hk, N, Dk = k.shape
-    ptrs, (P, H, page, D, mp, ts), dev = _kv8_args(cache, page_table, B)
-    _want_rows(k, "k", (B, H, N, D), dev)
-    _want_rows(v, "v", (B, H, N, D), dev)
+    B, _, N, _ = k.shape
+    dev, ptrs, (P, H, page, D), tab = _kv8_args(cache, page_table, B)
+    shape = (B, H, N, D)
+    kst, vst = _want_rows(k, "k", shape, dev), _want_rows(v, "v", shape, dev)
     _want(start, "start", torch.int32, (B,), dev)
+    cp = 0
     if counts is not None:
         _want(counts, "counts", torch.int32, (B,), dev)
+        cp = counts.data_ptr()
 
     def call(s):
-        st = tk_attn_kv8_write(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), *ptrs,
-                               start.data_ptr(), counts.data_ptr() if counts is not None else 0, B,
-                               H, N, D, P, page, mp, ts, s)
-        if st != TK_ATTN_OK:
+        st = library().tk_attn_kv8_write(k.data_ptr(), kst, v.data_ptr(), vst, *ptrs,
+                                         start.data_ptr(), cp, B, H, N, D, P, page, *tab, s)
+        if st:
             _raise_status("tk_attn_kv8_write", st)
 
-    _launch(k, stream, call)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _stream_on(dev, stream, call)
+    call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def kv8_read(cache: Kv8Cache, page_table, lengths, n: int | None = None, out_k=None, out_v=None,
@@ -960,27 +980,31 @@ def kv8_read(cache: Kv8Cache, page_table, lengths, n: int | None = None, out_k=N
     Enqueued on `stream`; returns immediately."""
     import torch
     B = page_table.shape[0] if page_table.dim() == 2 else -1
-    ptrs, (P, H, page, D, mp, ts), dev = _kv8_args(cache, page_table, B)
+    dev, ptrs, (P, H, page, D), tab = _kv8_args(cache, page_table, B)
     _want(lengths, "lengths", torch.int32, (B,), dev)
     if n is None:
         given = out_k if out_k is not None else out_v
         if given is None:
             raise ValueError("give n, or out_k and out_v")
-        n = int(given.shape[2]) if given.dim() == 4 else -1
-    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-        if t is not None:
-            _want(t, name, torch.bfloat16, (B, H, n, D), dev)
+        n = given.shape[2] if given.dim() == 4 else -1
+    shape = (B, H, n, D)
+    if out_k is not None:
+        _want(out_k, "out_k", torch.bfloat16, shape, dev)
+    if out_v is not None:
+        _want(out_v, "out_v", torch.bfloat16, shape, dev)
 
     def call(s):
-        ok, ov = (torch.zeros((B, H, n, D), dtype=torch.bfloat16, device=dev) if t is None else t
-                  for t in (out_k, out_v))
-        st = tk_attn_kv8_read(*ptrs, lengths.data_ptr(), ok.data_ptr(), ov.data_ptr(), B, H, n, D,
-                              P, page, mp, ts, s)
-        if st != TK_ATTN_OK:
+        ok, ov = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None
+                  else t for t in (out_k, out_v))
+        st = library().tk_attn_kv8_read(*ptrs, lengths.data_ptr(), ok.data_ptr(), ov.data_ptr(), B,
+                                        H, n, D, P, page, *tab, s)
+        if st:
             _raise_status("tk_attn_kv8_read", st)
         return ok, ov
 
-    return _launch(cache.k, stream, call)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _stream_on(dev, stream, call)
+    return call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def attention_forward_kv8(q, cache: Kv8Cache, page_table, lengths, counts=None,
@@ -996,37 +1020,44 @@ def attention_forward_kv8(q, cache: Kv8Cache, page_table, lengths, counts=None,
     are allocated by torch when not given.  Enqueued on `stream`; returns
     immediately."""
     import torch
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 CUDA tensor [B, H, Nq, D]")
-    B, H, Nq, Dq = q.shape
-    ptrs, (P, Hkv, page, D, mp, ts), dev = _kv8_args(cache, page_table, B)
-    if Dq != D or H % Hkv or q.device != dev:
-        raise ValueError(f"q must have the cache's head dim {D}, a multiple of its {Hkv} heads, "
-                         f"and be on {dev}")
+    qs = q.shape
+    if len(qs) != 4 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        _refuse(q, "q", "a contiguous bfloat16 CUDA tensor [B, H, Nq, D]")
+    B, H, Nq, Dq = qs
+    dev, ptrs, (P, Hkv, page, D), tab = _kv8_args(cache, page_table, B)
+    if Dq != D or H % Hkv or q.get_device() != dev:
+        _refuse(q, "q", f"of the cache's head dim {D}, a multiple of its {Hkv} heads, and on "
+                        f"cuda:{dev}")
     _want(lengths, "lengths", torch.int32, (B,), dev)
+    cp = 0
     if counts is not None:
         _want(counts, "counts", torch.int32, (B,), dev)
+        cp = counts.data_ptr()
     if out is not None:
-        _want(out, "out", torch.bfloat16, q.shape, dev)
+        _want(out, "out", torch.bfloat16, qs, dev)
     if lse is not None:
         _want(lse, "lse", torch.float32, (B, H, Nq), dev)
-    if workspace is not None and workspace.device != dev:
+    if workspace is not None and workspace.get_device() != dev:
         raise ValueError("the workspace must be on the tensors' device")
 
     def call(s):
+        lib, device = library(), q.device
         o = torch.empty_like(q) if out is None else out
-        ls = torch.empty((B, H, Nq), dtype=torch.float32, device=dev) if lse is None else lse
+        ls = torch.empty(qs[:3], dtype=torch.float32, device=device) if lse is None else lse
         ws = workspace
         if ws is None:
-            ws = torch.empty(tk_attn_fwd_kv8_workspace_bytes(B, H, Hkv, Nq, D), dtype=torch.uint8,
-                             device=dev)
-        st = tk_attn_fwd_kv8(q.data_ptr(), *ptrs, lengths.data_ptr(),
-                             counts.data_ptr() if counts is not None else 0, o.data_ptr(),
-                             ls.data_ptr(), B, H, Hkv, Nq, D, P, page, mp, ts,
-                             D ** -0.5 if scale is None else scale, int(bool(causal)),
-                             ws.data_ptr(), ws.numel() * ws.element_size(), s)
-        if st != TK_ATTN_OK:
+            ws_bytes = lib.tk_attn_fwd_kv8_workspace_bytes(B, H, Hkv, Nq, D)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        else:
+            ws_bytes = ws.numel() * ws.element_size()
+        st = lib.tk_attn_fwd_kv8(q.data_ptr(), *ptrs, lengths.data_ptr(), cp, o.data_ptr(),
+                                 ls.data_ptr(), B, H, Hkv, Nq, D, P, page, *tab,
+                                 D ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                 ws.data_ptr(), ws_bytes, s)
+        if st:
             _raise_status("tk_attn_fwd_kv8", st)
         return o, ls
 
-    return _launch(q, stream, call)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _stream_on(dev, stream, call)
+    return call(torch._C._cuda_getCurrentRawStream(dev))

@@ -118,9 +118,10 @@ extern "C" int tk_attn_kv8_write_check_args(
   if (st) return st;
   if (((uintptr_t)k | (uintptr_t)v) & 15u || ((uintptr_t)start | (uintptr_t)counts) & 3u)
     return TK_ATTN_ERR_UNSUPPORTED;
+  const int dims[3] = {B, Hkv, N};  // (the stride of a dimension of one says nothing)
   for (const long long *s : {k_strides, v_strides})
     for (int i = 0; i < 3; ++i)
-      if (s[i] < 0 || s[i] % 8 || s[i] >= (1LL << 40)) return TK_ATTN_ERR_UNSUPPORTED;
+      if (dims[i] > 1 && (s[i] < 0 || s[i] % 8 || s[i] >= (1LL << 40))) return TK_ATTN_ERR_UNSUPPORTED;
   if (B > 65535) return TK_ATTN_ERR_UNSUPPORTED;
   const size_t payload = (size_t)num_pages * Hkv * page * D, exps = (size_t)num_pages * Hkv;
   auto extent = [&](const long long *s) {

@@ -297,9 +297,13 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-bool strides_ok(const long long *s) {
+// (the stride of a dimension of one says nothing)
+bool strides_ok(const long long *s, int B, int H, int N) {
+  const int len[3] = {B, H, N};
   for (int i = 0; i < 3; ++i)
-    if (s[i] < 0 || s[i] % 8 || s[i] >= (1LL << 40)) return false;
+    if (len[i] == 1)
+      continue;
+    else if (s[i] < 0 || s[i] % 8 || s[i] >= (1LL << 40)) return false;
   return true;
 }
 
@@ -367,7 +371,7 @@ int check_common(const Call &c) {
   if ((uintptr_t)c.turns & 7u || (uintptr_t)c.positions & 3u ||
       ((uintptr_t)c.qw | (uintptr_t)c.kw) & (c.w_f32 ? 3u : 1u))
     return TK_ATTN_ERR_UNSUPPORTED;
-  if (!strides_ok(c.qs) || !strides_ok(c.ks)) return TK_ATTN_ERR_UNSUPPORTED;
+  if (!strides_ok(c.qs, c.B, c.H, c.N) || !strides_ok(c.ks, c.B, c.Hk, c.N)) return TK_ATTN_ERR_UNSUPPORTED;
   if ((long long)c.B * c.N > 0x7fffffffLL ||
       (long long)c.B * c.N * ((long long)c.H + c.Hk) >= (1LL << 40))
     return TK_ATTN_ERR_UNSUPPORTED;
@@ -516,8 +520,8 @@ extern "C" int tk_attn_qk_norm_rope_bwd_check_args(
        (uintptr_t)workspace) & 15u ||
       ((uintptr_t)dq_weight | (uintptr_t)dk_weight) & 3u)
     return TK_ATTN_ERR_UNSUPPORTED;
-  if (!strides_ok(dq_out_strides) || !strides_ok(dk_out_strides) || !strides_ok(dq_strides) ||
-      !strides_ok(dk_strides))
+  if (!strides_ok(dq_out_strides, B, H, N) || !strides_ok(dk_out_strides, B, Hk, N) ||
+      !strides_ok(dq_strides, B, H, N) || !strides_ok(dk_strides, B, Hk, N))
     return TK_ATTN_ERR_UNSUPPORTED;
   if (!distinct(dq_strides, B, H, N, D) || !distinct(dk_strides, B, Hk, N, D))
     return TK_ATTN_ERR_INVALID_ARG;

@@ -380,7 +380,8 @@ int tk_gemm_bf16_check_args(const void *a, const void *b, const void *c, int M, 
  *
  *   q, k        bf16 [B, H, N, D] and [B, Hk, N, D], any strides: *_strides
  *               holds the element strides of batch, head and token (host
- *               memory; >= 0, multiples of 8; the D values contiguous), so
+ *               memory; >= 0, multiples of 8, not looked at where the
+ *               dimension is 1; the D values contiguous), so
  *               the heads of a fused projection are read where they lie
  *   q_weight, k_weight   [D], bf16, or fp32 when weight_f32 != 0
  *   turns       [rot / 2] device, 8-byte aligned: frequency f_k in turns a
