@@ -6,6 +6,11 @@ streams.  The library is built in-tree (``attention_forward_tk_gb300/_build``)
 by :func:`attention_forward_tk_gb300.build.build_library`; if it is missing or
 fails to load, every call raises :class:`TkAttnError` -- there is no fallback.
 
+The helpers of the serving calls (``qk_norm_rope*``, ``kv8_*``,
+``attention_forward_kv8``) check, allocate and call in ``_tk_torch.so``
+(csrc/tk_torch.cpp, built by ``build_binding()``): at one token a sequence the
+marshalling done here would take longer than their kernels.
+
 The functions named ``tk_attn_*`` mirror the C entry points one for one and
 take raw integers (device addresses, sizes, a stream handle).  The
 ``attention_forward*`` helpers wrap them for torch tensors.
@@ -20,6 +25,7 @@ from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libtk_attn.so")
+BINDING_PATH = os.path.join(_HERE, "_build", "_tk_torch.so")
 
 TK_ATTN_OK = 0
 TK_ATTN_ERR_INVALID_ARG = -1
@@ -180,6 +186,37 @@ def library() -> ctypes.CDLL:
         return _lib
 
 
+_binding = None
+
+
+def binding():
+    """Load _tk_torch.so once: the compiled torch helpers, over the same library."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    library()
+    with _lock:
+        if _binding is None:
+            import importlib.machinery
+            import importlib.util
+
+            import torch  # noqa: F401  (the binding links torch's libraries)
+            if not os.path.exists(BINDING_PATH):
+                raise TkAttnError(
+                    f"{BINDING_PATH} is missing: build it with "
+                    "attention_forward_tk_gb300.build.build_binding()")
+            try:
+                loader = importlib.machinery.ExtensionFileLoader("_tk_torch", BINDING_PATH)
+                spec = importlib.util.spec_from_file_location("_tk_torch", BINDING_PATH,
+                                                              loader=loader)
+                mod = importlib.util.module_from_spec(spec)
+                loader.exec_module(mod)
+            except ImportError as e:  # pragma: no cover - depends on the machine
+                raise TkAttnError(f"cannot load {BINDING_PATH}: {e}") from e
+            _binding = mod
+    return _binding
+
+
 # ----------------------------------------------------------------- raw C calls
 
 
@@ -307,7 +344,7 @@ def tk_gemm_bf16_check_args(a: int, b: int, c: int, M: int, N: int, K: int) -> i
     return int(library().tk_gemm_bf16_check_args(a, b, c, M, N, K))
 
 
-_LL3, _LL4 = ctypes.c_longlong * 3, ctypes.c_longlong * 4
+_LL3 = ctypes.c_longlong * 3
 
 
 def _ll3(strides):
@@ -680,53 +717,25 @@ def attention_forward_host(q, k, v, causal: bool = False, scale: float | None = 
 
 
 # ----------------------------------------------------------------- a decoder's serving steps
-#
-# These are called for every layer of every token, and at one token a sequence
-# the device needs a few microseconds: the helpers below read each tensor
-# attribute once and build nothing that a check does not need.
 
 
-def _stream_on(dev, stream, call):
-    """call(stream handle) for tensors on CUDA device `dev`, with that device and
-    `stream` (a torch stream or a handle) current, so that what torch allocates
-    inside belongs to the stream that uses it.  stream None: torch's current
-    stream of that device."""
+def _on(stream, t, call):
+    """call() with `stream` (a torch stream or a handle) and its device current, so
+    that what torch allocates inside belongs to the stream that uses it."""
     import torch
-    with torch.cuda.device(dev):
-        if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", dev))
-        if stream.device.index != dev:
-            raise ValueError("the stream is on another device than the tensors")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+    dev = t.device
+    if dev.type != "cuda":
+        return call()  # (refused there)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError("the stream is on another device than the tensors")
+    with torch.cuda.stream(stream):
+        return call()
 
 
 def _raise_status(name: str, status: int):
     raise TkAttnError(f"{name}: {tk_attn_status_string(status)} ({status})", status)
-
-
-def _refuse(t, name, want):
-    raise ValueError(f"{name} must be {want}, not {str(t.dtype)[6:]} {list(t.shape)} with strides "
-                     f"{list(t.stride())} on {t.device}")
-
-
-def _want(t, name, dtype, shape, dev):
-    """t is a contiguous tensor of this type and shape on CUDA device dev."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(t, name, f"a contiguous {str(dtype)[6:]} tensor {list(shape)} on cuda:{dev}")
-
-
-def _want_rows(t, name, shape, dev):
-    """t is a bf16 tensor of this shape whose last dimension is contiguous; its
-    strides as the C calls take them."""
-    import torch
-    st = t.stride()
-    if t.dtype is not torch.bfloat16 or t.shape != shape or st[3] != 1 or t.get_device() != dev:
-        _refuse(t, name, f"a bfloat16 tensor {list(shape)} with a contiguous last dimension on "
-                         f"cuda:{dev}")
-    return _LL4(*st)
 
 
 def rope_turns(rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
@@ -752,35 +761,6 @@ def rope_turns(rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
     return torch.tensor(turns, dtype=torch.int64, device=device)
 
 
-def _norm_rope_args(q, k, q_weight, k_weight, turns, positions):
-    """(device, the C call's input arguments, (B, H, Hk, N, D, rot))."""
-    import torch
-    qs, ks = q.shape, k.shape
-    if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[2:] != ks[2:]:
-        raise ValueError("q must be [B, H, N, D] and k [B, Hk, N, D]")
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor")
-    B, H, N, D = qs
-    qst, kst = _want_rows(q, "q", qs, dev), _want_rows(k, "k", ks, dev)
-    wt = q_weight.dtype
-    f32 = wt is torch.float32
-    if not f32 and wt is not torch.bfloat16:
-        raise ValueError("q_weight and k_weight must be bfloat16 or float32")
-    _want(q_weight, "q_weight", wt, (D,), dev)
-    _want(k_weight, "k_weight", wt, (D,), dev)
-    rot = tp = pp = 0
-    if turns is not None:
-        rot = 2 * turns.numel()
-        _want(turns, "turns", torch.int64, (rot // 2,), dev)
-        tp = turns.data_ptr()
-    if positions is not None:
-        _want(positions, "positions", torch.int32, (B, N), dev)
-        pp = positions.data_ptr()
-    return dev, (q.data_ptr(), qst, k.data_ptr(), kst, q_weight.data_ptr(), k_weight.data_ptr(),
-                 f32, tp, pp), (B, H, ks[1], N, D, rot)
-
-
 def qk_norm_rope_forward(q, k, q_weight, k_weight, turns, positions=None, eps: float = 1e-6,
                          interleaved: bool = False, out_q=None, out_k=None, stream=None):
     """RMS norm of each head's query and key and the position rotation in one
@@ -792,30 +772,13 @@ def qk_norm_rope_forward(q, k, q_weight, k_weight, turns, positions=None, eps: f
     rotation); positions: int32 [B, N] (None: token i at i); interleaved: pair
     neighbours rather than halves.  Enqueued on `stream`; returns immediately.
     """
-    import torch
-    dev, ins, dims = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
-    if stream is not None or torch._C._cuda_getDevice() != dev:
-        return _stream_on(dev, stream, lambda s: _norm_rope_run(q, k, dev, ins, dims, eps,
-                                                                interleaved, out_q, out_k, s))
-    return _norm_rope_run(q, k, dev, ins, dims, eps, interleaved, out_q, out_k,
-                          torch._C._cuda_getCurrentRawStream(dev))
-
-
-def _norm_rope_run(q, k, dev, ins, dims, eps, interleaved, out_q, out_k, s):
-    import torch
-    if out_q is None:
-        out_q = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _want(out_q, "out_q", torch.bfloat16, q.shape, dev)
-    if out_k is None:
-        out_k = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _want(out_k, "out_k", torch.bfloat16, k.shape, dev)
-    st = library().tk_attn_qk_norm_rope(*ins, out_q.data_ptr(), out_k.data_ptr(), *dims,
-                                        1 if interleaved else 0, eps, s)
-    if st:
-        _raise_status("tk_attn_qk_norm_rope", st)
-    return out_q, out_k
+    def call():
+        return (_binding or binding()).norm_rope(q, k, q_weight, k_weight, turns, positions, eps,
+                                                 interleaved, out_q, out_k)
+    r = call() if stream is None else _on(stream, q, call)
+    if type(r) is int:
+        _raise_status("tk_attn_qk_norm_rope", r)
+    return r
 
 
 def qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out, dk_out, positions=None,
@@ -826,34 +789,14 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, turns, dq_out, dk_out, posit
     dk_weight) in fp32 [D].  dq_out and dk_out: bf16, last dimension contiguous.
     Equal calls give equal bits.  Enqueued on `stream`; returns immediately.
     """
-    import torch
-    dev, ins, dims = _norm_rope_args(q, k, q_weight, k_weight, turns, positions)
-    gos = (dq_out.data_ptr(), _want_rows(dq_out, "dq_out", q.shape, dev), dk_out.data_ptr(),
-           _want_rows(dk_out, "dk_out", k.shape, dev))
-    if workspace is not None and workspace.get_device() != dev:
-        raise ValueError("the workspace must be on the tensors' device")
-
-    def call(s):
-        D = dims[4]
-        gq = torch.empty_like(q) if dq is None else dq
-        gk = torch.empty_like(k) if dk is None else dk
-        gw = torch.empty((2, D), dtype=torch.float32, device=q.device)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(tk_attn_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
-                             device=q.device)
-        gp = gw.data_ptr()
-        st = library().tk_attn_qk_norm_rope_bwd(
-            *ins, *gos, gq.data_ptr(), _want_rows(gq, "dq", q.shape, dev), gk.data_ptr(),
-            _want_rows(gk, "dk", k.shape, dev), gp, gp + 4 * D, *dims, 1 if interleaved else 0,
-            eps, ws.data_ptr(), ws.numel() * ws.element_size(), s)
-        if st:
-            _raise_status("tk_attn_qk_norm_rope_bwd", st)
-        return gq, gk, gw[0], gw[1]
-
-    if stream is not None or torch._C._cuda_getDevice() != dev:
-        return _stream_on(dev, stream, call)
-    return call(torch._C._cuda_getCurrentRawStream(dev))
+    def call():
+        return (_binding or binding()).norm_rope_bwd(q, k, q_weight, k_weight, turns, positions,
+                                                     eps, interleaved, dq_out, dk_out, dq, dk,
+                                                     workspace)
+    r = call() if stream is None else _on(stream, q, call)
+    if type(r) is int:
+        _raise_status("tk_attn_qk_norm_rope_bwd", r)
+    return r
 
 
 _norm_rope_fn = None
@@ -919,56 +862,17 @@ def kv8_cache(num_pages: int, heads: int, page: int, head_dim: int, device="cuda
                     torch.zeros(shape[:2], dtype=torch.int8, device=device))
 
 
-def _kv8_args(cache, page_table, B):
-    """(device, the C calls' pointers, (num_pages, Hkv, page, D), (max_pages,
-    table stride)) of a cache and its page tables."""
-    import torch
-    k, v, ke, ve = cache
-    shape, f8, i8 = k.shape, torch.float8_e4m3fn, torch.int8
-    dev = k.get_device()
-    if len(shape) != 4 or k.dtype is not f8 or dev < 0 or not k.is_contiguous():
-        _refuse(k, "the cache's k", "a contiguous float8_e4m3fn CUDA tensor [pages, heads, page, D]")
-    _want(v, "the cache's v", f8, shape, dev)
-    _want(ke, "the cache's k_exp", i8, shape[:2], dev)
-    _want(ve, "the cache's v_exp", i8, shape[:2], dev)
-    ts, st = page_table.shape, page_table.stride()
-    if page_table.dtype is not torch.int32 or len(ts) != 2 or ts[0] != B or \
-            (st[1] != 1 and ts[1] != 1) or page_table.get_device() != dev:
-        _refuse(page_table, "page_table", f"an int32 tensor [{B}, pages] with contiguous rows on "
-                                          f"cuda:{dev}")
-    # (one sequence's table has no row stride of its own)
-    return dev, (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr(),
-                 page_table.data_ptr()), shape, (ts[1], st[0] if B > 1 else ts[1])
-
-
 def kv8_write(cache: Kv8Cache, k, v, page_table, start, counts=None, stream=None) -> None:
     """Append rows to the cache: row i < counts[b] of k and v (bf16
     [B, Hkv, N, D], last dimension contiguous) goes to position start[b] + i of
     sequence b, quantised with the scale of its page and head.  start, counts:
     int32 [B]; page_table: int32 [B, pages].  Enqueued on `stream`; returns
     immediately."""
-    import torch
-    if k.dim() != 4:
-        raise ValueError("k must be [B, Hkv, N, D]")
-    B, _, N, _ = k.shape
-    dev, ptrs, (P, H, page, D), tab = _kv8_args(cache, page_table, B)
-    shape = (B, H, N, D)
-    kst, vst = _want_rows(k, "k", shape, dev), _want_rows(v, "v", shape, dev)
-    _want(start, "start", torch.int32, (B,), dev)
-    cp = 0
-    if counts is not None:
-        _want(counts, "counts", torch.int32, (B,), dev)
-        cp = counts.data_ptr()
-
-    def call(s):
-        st = library().tk_attn_kv8_write(k.data_ptr(), kst, v.data_ptr(), vst, *ptrs,
-                                         start.data_ptr(), cp, B, H, N, D, P, page, *tab, s)
-        if st:
-            _raise_status("tk_attn_kv8_write", st)
-
-    if stream is not None or torch._C._cuda_getDevice() != dev:
-        return _stream_on(dev, stream, call)
-    call(torch._C._cuda_getCurrentRawStream(dev))
+    def call():
+        return (_binding or binding()).kv8_write(cache, k, v, page_table, start, counts)
+    r = call() if stream is None else _on(stream, k, call)
+    if r:
+        _raise_status("tk_attn_kv8_write", r)
 
 
 def kv8_read(cache: Kv8Cache, page_table, lengths, n: int | None = None, out_k=None, out_v=None,
@@ -978,33 +882,12 @@ def kv8_read(cache: Kv8Cache, page_table, lengths, n: int | None = None, out_k=N
     them.  Rows past a sequence's length are left as they were (zero where this
     allocates).  n defaults to out_k's, and must be given without out_k and out_v.
     Enqueued on `stream`; returns immediately."""
-    import torch
-    B = page_table.shape[0] if page_table.dim() == 2 else -1
-    dev, ptrs, (P, H, page, D), tab = _kv8_args(cache, page_table, B)
-    _want(lengths, "lengths", torch.int32, (B,), dev)
-    if n is None:
-        given = out_k if out_k is not None else out_v
-        if given is None:
-            raise ValueError("give n, or out_k and out_v")
-        n = given.shape[2] if given.dim() == 4 else -1
-    shape = (B, H, n, D)
-    if out_k is not None:
-        _want(out_k, "out_k", torch.bfloat16, shape, dev)
-    if out_v is not None:
-        _want(out_v, "out_v", torch.bfloat16, shape, dev)
-
-    def call(s):
-        ok, ov = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None
-                  else t for t in (out_k, out_v))
-        st = library().tk_attn_kv8_read(*ptrs, lengths.data_ptr(), ok.data_ptr(), ov.data_ptr(), B,
-                                        H, n, D, P, page, *tab, s)
-        if st:
-            _raise_status("tk_attn_kv8_read", st)
-        return ok, ov
-
-    if stream is not None or torch._C._cuda_getDevice() != dev:
-        return _stream_on(dev, stream, call)
-    return call(torch._C._cuda_getCurrentRawStream(dev))
+    def call():
+        return (_binding or binding()).kv8_read(cache, page_table, lengths, n, out_k, out_v)
+    r = call() if stream is None else _on(stream, cache.k, call)
+    if type(r) is int:
+        _raise_status("tk_attn_kv8_read", r)
+    return r
 
 
 def attention_forward_kv8(q, cache: Kv8Cache, page_table, lengths, counts=None,
@@ -1019,45 +902,10 @@ def attention_forward_kv8(q, cache: Kv8Cache, page_table, lengths, counts=None,
     A row that sees nothing gets O = 0 and LSE = -inf.  Outputs and the workspace
     are allocated by torch when not given.  Enqueued on `stream`; returns
     immediately."""
-    import torch
-    qs = q.shape
-    if len(qs) != 4 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
-        _refuse(q, "q", "a contiguous bfloat16 CUDA tensor [B, H, Nq, D]")
-    B, H, Nq, Dq = qs
-    dev, ptrs, (P, Hkv, page, D), tab = _kv8_args(cache, page_table, B)
-    if Dq != D or H % Hkv or q.get_device() != dev:
-        _refuse(q, "q", f"of the cache's head dim {D}, a multiple of its {Hkv} heads, and on "
-                        f"cuda:{dev}")
-    _want(lengths, "lengths", torch.int32, (B,), dev)
-    cp = 0
-    if counts is not None:
-        _want(counts, "counts", torch.int32, (B,), dev)
-        cp = counts.data_ptr()
-    if out is not None:
-        _want(out, "out", torch.bfloat16, qs, dev)
-    if lse is not None:
-        _want(lse, "lse", torch.float32, (B, H, Nq), dev)
-    if workspace is not None and workspace.get_device() != dev:
-        raise ValueError("the workspace must be on the tensors' device")
-
-    def call(s):
-        lib, device = library(), q.device
-        o = torch.empty_like(q) if out is None else out
-        ls = torch.empty(qs[:3], dtype=torch.float32, device=device) if lse is None else lse
-        ws = workspace
-        if ws is None:
-            ws_bytes = lib.tk_attn_fwd_kv8_workspace_bytes(B, H, Hkv, Nq, D)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-        else:
-            ws_bytes = ws.numel() * ws.element_size()
-        st = lib.tk_attn_fwd_kv8(q.data_ptr(), *ptrs, lengths.data_ptr(), cp, o.data_ptr(),
-                                 ls.data_ptr(), B, H, Hkv, Nq, D, P, page, *tab,
-                                 D ** -0.5 if scale is None else scale, 1 if causal else 0,
-                                 ws.data_ptr(), ws_bytes, s)
-        if st:
-            _raise_status("tk_attn_fwd_kv8", st)
-        return o, ls
-
-    if stream is not None or torch._C._cuda_getDevice() != dev:
-        return _stream_on(dev, stream, call)
-    return call(torch._C._cuda_getCurrentRawStream(dev))
+    def call():
+        return (_binding or binding()).kv8_attend(q, cache, page_table, lengths, counts, causal,
+                                                  scale, out, lse, workspace)
+    r = call() if stream is None else _on(stream, q, call)
+    if type(r) is int:
+        _raise_status("tk_attn_fwd_kv8", r)
+    return r

@@ -131,8 +131,17 @@ def test_kv8_without_a_gpu_reports_arch(tk_lib):
     assert tk_lib.tk_attn_fwd_kv8_workspace_bytes(2, 4, 2, 3, 64) == 0
 
 
-def test_helpers_refuse_cpu_tensors_and_wrong_shapes():
+def test_binding_raises_when_missing(tk_lib, monkeypatch):
+    monkeypatch.setattr(tk_lib, "_binding", None)
+    monkeypatch.setattr(tk_lib, "BINDING_PATH", "/nonexistent/_tk_torch.so")
+    with pytest.raises(tk_lib.TkAttnError):
+        tk_lib.binding()
+
+
+def test_helpers_refuse_cpu_tensors_and_wrong_shapes(tk_lib):
     import torch
+    from attention_forward_tk_gb300.build import build_binding
+    build_binding()
     import attention_forward_tk_gb300 as tk
     x = torch.zeros((1, 2, 3, 64), dtype=torch.bfloat16)
     w = torch.ones(64, dtype=torch.bfloat16)
