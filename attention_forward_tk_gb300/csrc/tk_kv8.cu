@@ -97,6 +97,15 @@ int log2i(int x) {
   return l;
 }
 
+// (a thread's registers hold its part of a whole page)
+template <int kPage>
+void launch_write(const Kv8WriteParams &p, int D, dim3 grid, cudaStream_t s) {
+  if (D == 64)
+    tk_kv8_write_kernel<64, kPage><<<grid, kKv8Threads, 0, s>>>(p);
+  else
+    tk_kv8_write_kernel<128, kPage><<<grid, kKv8Threads, 0, s>>>(p);
+}
+
 size_t table_bytes(int B, int max_pages, int table_stride) {
   return ((size_t)(B - 1) * table_stride + max_pages) * 4;
 }
@@ -169,10 +178,12 @@ extern "C" int tk_attn_kv8_write(const void *k, const long long *k_strides, cons
   p.err = dv.err_word;
   const dim3 grid(kv8_span(N, page), 2 * Hkv, B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 64)
-    tk_kv8_write_kernel<64><<<grid, kKv8Threads, 0, s>>>(p);
-  else
-    tk_kv8_write_kernel<128><<<grid, kKv8Threads, 0, s>>>(p);
+  switch (page) {
+    case 16: launch_write<16>(p, D, grid, s); break;
+    case 32: launch_write<32>(p, D, grid, s); break;
+    case 64: launch_write<64>(p, D, grid, s); break;
+    default: launch_write<128>(p, D, grid, s); break;
+  }
   return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }
 

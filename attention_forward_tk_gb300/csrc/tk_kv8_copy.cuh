@@ -58,15 +58,25 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// bf16x2 times 2^-e, to two codes; infinities to NaN (`odd`: the block holds
-// a non-finite value).
-__device__ __forceinline__ uint32_t quant2(uint32_t v, float s, bool odd) {
-  float a = __uint_as_float(v << 16), b = __uint_as_float(v & 0xffff0000u);
-  if (odd) {
-    if ((v & 0x7fffu) == 0x7f80u) a = __uint_as_float(0x7fc00000u);
-    if ((v & 0x7fff0000u) == 0x7f800000u) b = __uint_as_float(0x7fc00000u);
-  }
-  return pack_e4m3x2(a * s, b * s);
+// Four bf16 values times 2^-e, to four codes.
+__device__ __forceinline__ uint32_t quant4(uint32_t v, uint32_t w, float s) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(__uint_as_float(v << 16) * s), "f"(__uint_as_float(v & 0xffff0000u) * s),
+        "f"(__uint_as_float(w << 16) * s), "f"(__uint_as_float(w & 0xffff0000u) * s));
+  return r;
+}
+
+// Infinities of a bf16x2 to NaN (E4M3 has none, and the conversion would make
+// them the largest value).
+__device__ __forceinline__ uint32_t inf_to_nan(uint32_t v) {
+  if ((v & 0x7fffu) == 0x7f80u) v |= 0x40u;
+  if ((v & 0x7fff0000u) == 0x7f800000u) v |= 0x400000u;
+  return v;
 }
 
 // Largest finite magnitude of a bf16x2's two halves, as bits.
@@ -87,11 +97,12 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
 }
 
 // grid: (pages a write can touch, 2 * Hkv, B)
-template <int D>
+template <int D, int kPage>
 __global__ void __launch_bounds__(kKv8Threads)
     tk_kv8_write_kernel(const __grid_constant__ Kv8WriteParams p) {
-  constexpr int kVec = D / 8;                       // 16-byte loads a row
-  constexpr int kMaxVec = 128 * kVec / kKv8Threads;  // a thread's loads of a 128-row page
+  constexpr int kVec = D / 8;                          // 16-byte loads a row
+  constexpr int kMaxVec = kPage * kVec / kKv8Threads;  // a thread's loads of a whole page
+  constexpr int kRowsStep = kKv8Threads / kVec;        // rows from one of them to the next
   __shared__ uint32_t red[kKv8Threads / 32];
   const Kv8Geom &g = p.g;
   const int b = blockIdx.z;
@@ -103,24 +114,25 @@ __global__ void __launch_bounds__(kKv8Threads)
   if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
     atomicCAS(p.err, 0, kDevErrIndex);
   if (n == 0) return;
-  const int slot = start / g.page + blockIdx.x;
-  const long long at = (long long)slot * g.page;
+  const int slot = start / kPage + blockIdx.x;
+  const long long at = (long long)slot * kPage;
   if (at >= start + n) return;
   const int first = (int)at;                // position of the page's row 0
   const int r0 = max(start - first, 0);     // the page's new rows are [r0, r1)
-  const int r1 = min(start + n - first, g.page);
+  const int r1 = min(start + n - first, kPage);
   const int id = p.table[kv8_table_offset(g, b, slot)];
   // the new rows, in registers
-  const __nv_bfloat16 *src =
-      p.src[which] + b * p.sb[which] + h * p.sh[which] + (long long)(first + r0 - start) * p.sn[which];
-  const int nvec = (r1 - r0) * kVec;
+  const int row = threadIdx.x / kVec, col = threadIdx.x % kVec;  // this thread's first piece
+  const long long step = kRowsStep * p.sn[which];
+  const __nv_bfloat16 *src = p.src[which] + b * p.sb[which] + h * p.sh[which] +
+                             (long long)(first + r0 - start + row) * p.sn[which] + col * 8;
+  const int rows = r1 - r0;
   uint4 v[kMaxVec];
 #pragma unroll
   for (int i = 0; i < kMaxVec; ++i) {
-    const int c = threadIdx.x + i * kKv8Threads;
-    v[i] = c < nvec ? *reinterpret_cast<const uint4 *>(src + (c / kVec) * p.sn[which] +
-                                                       (c % kVec) * 8)
-                    : make_uint4(0, 0, 0, 0);
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (row + i * kRowsStep < rows) v[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+    src += step;
   }
   if (!kv8_page_ok(g, id)) {
     if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevErrIndex);
@@ -147,12 +159,12 @@ __global__ void __launch_bounds__(kKv8Threads)
     m = block_max(m, red);
   }
   const int e = max(kv8_exponent(m), held);
-  uint8_t *rows = p.payload[which] + kv8_row_offset(g, id, h, 0);
+  uint8_t *page = p.payload[which] + kv8_row_offset(g, id, h, 0);
   if (threadIdx.x == 0) p.exps[which][eoff] = (int8_t)e;
   if (held > -128 && e > held) {
     // rows that stay, onto the new grid
     const float s = exp2i(max(held - e, -126));
-    uint2 *old = reinterpret_cast<uint2 *>(rows);
+    uint2 *old = reinterpret_cast<uint2 *>(page);
     for (int c = threadIdx.x; c < r0 * kVec; c += kKv8Threads) {
       uint2 w = old[c];
       uint32_t *q = reinterpret_cast<uint32_t *>(&w);
@@ -166,14 +178,21 @@ __global__ void __launch_bounds__(kKv8Threads)
     }
   }
   const float s = exp2i(max(-e, -126));
-  uint2 *dst = reinterpret_cast<uint2 *>(rows + r0 * D);
+  uint2 *dst = reinterpret_cast<uint2 *>(page + r0 * D) + threadIdx.x;
+  if (odd) {  // infinities become NaN before the scaling
 #pragma unroll
-  for (int i = 0; i < kMaxVec; ++i) {
-    const int c = threadIdx.x + i * kKv8Threads;
-    if (c < nvec)
-      dst[c] = make_uint2(quant2(v[i].x, s, odd) | quant2(v[i].y, s, odd) << 16,
-                          quant2(v[i].z, s, odd) | quant2(v[i].w, s, odd) << 16);
+    for (int i = 0; i < kMaxVec; ++i) {
+      v[i].x = inf_to_nan(v[i].x);
+      v[i].y = inf_to_nan(v[i].y);
+      v[i].z = inf_to_nan(v[i].z);
+      v[i].w = inf_to_nan(v[i].w);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < kMaxVec; ++i)
+    if (row + i * kRowsStep < rows)
+      dst[i * kKv8Threads] =
+          make_uint2(quant4(v[i].x, v[i].y, s), quant4(v[i].z, v[i].w, s));
 }
 
 struct Kv8ReadParams {

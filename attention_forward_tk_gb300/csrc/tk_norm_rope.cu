@@ -17,8 +17,9 @@
 // Mapping: D/8 lanes own a head row, eight values each, in two groups of four
 // placed so that a pair's two values sit in one lane (no exchange for the
 // rotation; three or four shuffles for the mean).  A row group keeps one
-// token's sines and cosines for `hpg` consecutive heads; the groups of a block
-// take consecutive tokens, so a block writes runs of consecutive rows of a head-major output.
+// token's sines and cosines, multiplied by the weights, for `hpg` consecutive
+// heads; the groups of a block take consecutive tokens, so a block writes runs
+// of consecutive rows of a head-major output.
 // Everything is computed in fp32 and rounded once to bf16.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,8 +36,9 @@ namespace tkattn {
 namespace {
 
 constexpr int kNrThreads = 256;
-// Backward: blocks each keep one row of partial weight gradients.
-constexpr int kNrBwdMaxBlocks = 1024;
+constexpr int kNrFwdHeads = 16, kNrBwdHeads = 8;  // heads a row group takes for one token, at most
+// Rows of partial weight gradients: one for each block of the backward.
+constexpr int kNrBwdMaxBlocks = 2048;
 
 struct NrTensor {
   const __nv_bfloat16 *p;
@@ -54,18 +56,17 @@ struct NrParams {
   const int *pos;  // [B, N] or null: 0 .. N-1
   float eps;
   int B, N, H[2], rot;
-  int hpg;             // heads a row group takes for one token
-  int chunks[2];       // ceil(H / hpg)
-  long long items;     // (chunks[0] + chunks[1]) * token tiles
-  long long tiles;     // ceil(B * N / groups per block)
-  float *dw_part;      // [gridDim.x, 2, D]
+  int hpg;          // heads a row group takes for one token
+  int chunks[2];    // ceil(H / hpg): gridDim.y of the two together
+  int tiles;        // ceil(B * N / groups per block)
+  float *dw_part;   // [gridDim.y * gridDim.x, D]: the queries' rows, then the keys'
 };
 
-// Element index of a lane's two groups of four: pairs (lo + i, hi + i) when the
-// halves are paired, (lo, lo+1), (lo+2, lo+3), (hi, ..) when interleaved or
-// past the rotated values.
-__device__ __forceinline__ void lane_cols(int l, int rot, bool inter, int &lo, int &hi) {
-  if (!inter && l < rot / 8) {
+// First columns of a lane's two groups of four: pair i is (lo + i, hi + i) when
+// halves are paired; neighbours when interleaved; past the rotated values
+// eight in a row either way.
+__device__ __forceinline__ void lane_cols(int l, int rot, bool halves, int &lo, int &hi) {
+  if (halves && l < rot / 8) {
     lo = 4 * l;
     hi = rot / 2 + 4 * l;
   } else {
@@ -74,35 +75,57 @@ __device__ __forceinline__ void lane_cols(int l, int rot, bool inter, int &lo, i
   }
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *row, int lo, int hi, uint2 &a,
-                                      uint2 &b) {
-  a = *reinterpret_cast<const uint2 *>(row + lo);
-  b = *reinterpret_cast<const uint2 *>(row + hi);
+struct Raw {  // eight bf16 values as loaded
+  uint2 lo, hi;
+};
+
+__device__ __forceinline__ Raw load8(const __nv_bfloat16 *row, int lo, int hi) {
+  Raw r;
+  r.lo = __ldg(reinterpret_cast<const uint2 *>(row + lo));
+  r.hi = __ldg(reinterpret_cast<const uint2 *>(row + hi));
+  return r;
 }
 
-__device__ __forceinline__ void widen8(uint2 a, uint2 b, float (&v)[8]) {
-  const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The lane's four pairs (a, b): across the two groups, or neighbours.
+template <bool kHalves>
+__device__ __forceinline__ void pairs_of(const Raw &r, float (&a)[4], float (&b)[4]) {
+  if constexpr (kHalves) {
+    a[0] = bf_lo(r.lo.x), a[1] = bf_hi(r.lo.x), a[2] = bf_lo(r.lo.y), a[3] = bf_hi(r.lo.y);
+    b[0] = bf_lo(r.hi.x), b[1] = bf_hi(r.hi.x), b[2] = bf_lo(r.hi.y), b[3] = bf_hi(r.hi.y);
+  } else {
+    a[0] = bf_lo(r.lo.x), b[0] = bf_hi(r.lo.x), a[1] = bf_lo(r.lo.y), b[1] = bf_hi(r.lo.y);
+    a[2] = bf_lo(r.hi.x), b[2] = bf_hi(r.hi.x), a[3] = bf_lo(r.hi.y), b[3] = bf_hi(r.hi.y);
   }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *row, int lo, int hi, const float (&v)[8]) {
-  *reinterpret_cast<uint2 *>(row + lo) =
-      make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-  *reinterpret_cast<uint2 *>(row + hi) =
-      make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+template <bool kHalves>
+__device__ __forceinline__ void store8(__nv_bfloat16 *row, int lo, int hi, const float (&a)[4],
+                                       const float (&b)[4]) {
+  uint2 x, y;
+  if constexpr (kHalves) {
+    x = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    y = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+  } else {
+    x = make_uint2(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]));
+    y = make_uint2(pack_bf16x2(a[2], b[2]), pack_bf16x2(a[3], b[3]));
+  }
+  *reinterpret_cast<uint2 *>(row + lo) = x;
+  *reinterpret_cast<uint2 *>(row + hi) = y;
 }
 
-__device__ __forceinline__ void load_w(const void *w, int f32, int lo, int hi, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = (i < 4 ? lo : hi) + (i & 3);
-    v[i] = f32 ? static_cast<const float *>(w)[c]
-               : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c]);
-  }
+// Column of a lane's value i of the first (a) or second (b) of its pairs.
+template <bool kHalves>
+__device__ __forceinline__ int pair_col(int lo, int hi, int i, int second) {
+  if constexpr (kHalves) return (second ? hi : lo) + i;
+  return (i < 2 ? lo : hi) + 2 * (i & 1) + second;
+}
+
+__device__ __forceinline__ float weight_at(const void *w, int f32, int c) {
+  return f32 ? static_cast<const float *>(w)[c]
+             : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c]);
 }
 
 // cos and sin of a lane's four pairs at position p.
@@ -123,20 +146,6 @@ __device__ __forceinline__ void lane_angles(const uint64_t *turns, int l, int p,
   }
 }
 
-// Turn the lane's pairs by (cs, sn): kHalf pairs v[i] with v[4 + i], else
-// neighbours.
-template <bool kHalves>
-__device__ __forceinline__ void turn8(float (&v)[8], const float (&cs)[4], const float (&sn)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float &a = v[kHalves ? i : 2 * i];
-    float &b = v[kHalves ? 4 + i : 2 * i + 1];
-    const float x = a, y = b;
-    a = x * cs[i] - y * sn[i];
-    b = y * cs[i] + x * sn[i];
-  }
-}
-
 template <int kLanes>
 __device__ __forceinline__ float group_sum(float s) {
 #pragma unroll
@@ -144,10 +153,10 @@ __device__ __forceinline__ float group_sum(float s) {
   return s;
 }
 
-// One item = one token tile (a token for each row group of the block) x one
-// run of hpg heads of the queries or the keys.
+// grid: (token tiles, or fewer blocks that step over them; runs of hpg heads,
+// the queries' first).  A block takes one token for each of its row groups.
 template <int D, bool kHalves, bool kBwd>
-__global__ void __launch_bounds__(kNrThreads)
+__global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4)
     tk_norm_rope_kernel(const __grid_constant__ NrParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kNrThreads / kLanes;
@@ -155,145 +164,168 @@ __global__ void __launch_bounds__(kNrThreads)
   const int l = threadIdx.x % kLanes;
   const int grp = threadIdx.x / kLanes;
   int lo, hi;
-  lane_cols(l, p.rot, !kHalves, lo, hi);
+  lane_cols(l, p.rot, kHalves, lo, hi);
   const bool turned = 8 * l < p.rot;
-  float dw[2][8];
-  if constexpr (kBwd) {
+  const int which = (int)blockIdx.y >= p.chunks[0];
+  const int h0 = ((int)blockIdx.y - (which ? p.chunks[0] : 0)) * p.hpg;
+  const int h1 = min(h0 + p.hpg, p.H[which]);
+  const NrTensor X = p.x[which];
+  const long long yh = p.yh[which];
+  float wa[4], wb[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    wa[i] = weight_at(p.w[which], p.w_f32, pair_col<kHalves>(lo, hi, i, 0));
+    wb[i] = weight_at(p.w[which], p.w_f32, pair_col<kHalves>(lo, hi, i, 1));
   }
-  const long long tokens = (long long)p.B * p.N;
-  for (long long it = blockIdx.x; it < p.items; it += gridDim.x) {
-    const int nchunk = p.chunks[0] + p.chunks[1];
-    const long long tile = it / nchunk;
-    int ch = (int)(it - tile * nchunk);
-    const int which = ch >= p.chunks[0];
-    if (which) ch -= p.chunks[0];
-    const long long tok = tile * kGroups + grp;
+  float da[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};  // backward: sums of g o n
+  const unsigned tokens = (unsigned)p.B * (unsigned)p.N;
+  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const unsigned tok = (unsigned)tile * kGroups + grp;
     const bool live = tok < tokens;
-    const int b = live ? (int)(tok / p.N) : 0;
-    const int n = live ? (int)(tok - (long long)b * p.N) : 0;
+    const int b = live ? (int)(tok / (unsigned)p.N) : 0;
+    const int n = live ? (int)(tok - (unsigned)b * (unsigned)p.N) : 0;
+    const __nv_bfloat16 *xrow = X.p + b * X.sb + n * X.sn + h0 * X.sh;
+    __nv_bfloat16 *yrow = p.y[which] + b * p.yb[which] + n * p.yn[which] + h0 * yh;
+    const int end = live ? h1 - h0 : 0;  // heads this group has
     float cs[4], sn[4];
-    const int pos = p.pos ? p.pos[(long long)b * p.N + n] : n;
-    lane_angles(p.turns, l, pos, turned, cs, sn);
-    if constexpr (kBwd) {
+    lane_angles(p.turns, l, p.pos ? p.pos[live ? tok : 0] : n, turned, cs, sn);
+    if constexpr (!kBwd) {
+      // y_a = r (a wa cos - b wb sin), y_b = r (b wb cos + a wa sin)
+      float ca[4], sa[4], cb[4], sb[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sn[i] = -sn[i];  // the rotation's transpose
-    }
-    float w[8];
-    load_w(p.w[which], p.w_f32, lo, hi, w);
-    const NrTensor &X = p.x[which];
-    const __nv_bfloat16 *xrow = X.p + b * X.sb + n * X.sn;
-    __nv_bfloat16 *yrow = p.y[which] + b * p.yb[which] + n * p.yn[which];
-    float sum[8];  // backward: this item's g o n
-    if constexpr (kBwd) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-    }
-    const int h0 = ch * p.hpg;
-    const int h1 = min(h0 + p.hpg, p.H[which]);
-    for (int h = h0; h < h1; h += kUnroll) {
-      uint2 xa[kUnroll], xb[kUnroll], ga[kUnroll], gb[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        xa[u] = xb[u] = make_uint2(0, 0);
-        if (live && h + u < h1) load8(xrow + (h + u) * X.sh, lo, hi, xa[u], xb[u]);
-        if constexpr (kBwd) {
-          const NrTensor &G = p.dy[which];
-          ga[u] = gb[u] = make_uint2(0, 0);
-          if (live && h + u < h1)
-            load8(G.p + b * G.sb + n * G.sn + (h + u) * G.sh, lo, hi, ga[u], gb[u]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        ca[i] = wa[i] * cs[i];
+        sa[i] = wa[i] * sn[i];
+        cb[i] = wb[i] * cs[i];
+        sb[i] = -wb[i] * sn[i];
       }
+      for (int h = 0; h < h1 - h0; h += kUnroll) {
+        Raw x[kUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        float v[8];
-        widen8(xa[u], xb[u], v);
-        float ss = 0.f;
+        for (int u = 0; u < kUnroll; ++u) {
+          x[u].lo = x[u].hi = make_uint2(0, 0);
+          if (h + u < end) x[u] = load8(xrow + u * X.sh, lo, hi);
+        }
+        xrow += kUnroll * X.sh;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-        ss = group_sum<kLanes>(ss);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const bool store = live && h + u < h1;
-        if constexpr (!kBwd) {
+        for (int u = 0; u < kUnroll; ++u) {
+          float a[4], c[4];
+          pairs_of<kHalves>(x[u], a, c);
+          float ss = 0.f, s2 = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
-          if (turned) turn8<kHalves>(v, cs, sn);
-          if (store) store8(yrow + (h + u) * p.yh[which], lo, hi, v);
-        } else {
-          float g[8];
-          widen8(ga[u], gb[u], g);
-          if (turned) turn8<kHalves>(g, cs, sn);
-          float dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] *= r;  // n
-            if (store) sum[i] = fmaf(g[i], v[i], sum[i]);
-            g[i] *= w[i];
-            dot = fmaf(g[i], v[i], dot);
+          for (int i = 0; i < 4; ++i) {
+            ss = fmaf(a[i], a[i], ss);
+            s2 = fmaf(c[i], c[i], s2);
           }
-          dot = group_sum<kLanes>(dot) * (1.f / D);
+          ss = group_sum<kLanes>(ss + s2);
+          const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+          float ya[4], yb[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = r * (g[i] - v[i] * dot);
-          if (store) store8(yrow + (h + u) * p.yh[which], lo, hi, g);
+          for (int i = 0; i < 4; ++i) {
+            ya[i] = fmaf(a[i], ca[i], c[i] * sb[i]) * r;
+            yb[i] = fmaf(c[i], cb[i], a[i] * sa[i]) * r;
+          }
+          if (h + u < end) store8<kHalves>(yrow + u * yh, lo, hi, ya, yb);
         }
+        yrow += kUnroll * yh;
       }
-    }
-    if constexpr (kBwd) {
-      if (which) {
+    } else {
+      const NrTensor G = p.dy[which];
+      const __nv_bfloat16 *grow = G.p + b * G.sb + n * G.sn + h0 * G.sh;
+      for (int h = 0; h < h1 - h0; h += kUnroll) {
+        Raw x[kUnroll], y[kUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[1][i] += sum[i];
-      } else {
+        for (int u = 0; u < kUnroll; ++u) {
+          x[u].lo = x[u].hi = y[u].lo = y[u].hi = make_uint2(0, 0);
+          if (h + u < end) {
+            x[u] = load8(xrow + u * X.sh, lo, hi);
+            y[u] = load8(grow + u * G.sh, lo, hi);
+          }
+        }
+        xrow += kUnroll * X.sh;
+        grow += kUnroll * G.sh;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[0][i] += sum[i];
+        for (int u = 0; u < kUnroll; ++u) {
+          float a[4], c[4], ga[4], gb[4];
+          pairs_of<kHalves>(x[u], a, c);
+          pairs_of<kHalves>(y[u], ga, gb);
+          float ss = 0.f, dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // the rotation's transpose
+            const float ta = fmaf(ga[i], cs[i], gb[i] * sn[i]);
+            const float tb = fmaf(gb[i], cs[i], -ga[i] * sn[i]);
+            ga[i] = ta;
+            gb[i] = tb;
+            ss = fmaf(a[i], a[i], fmaf(c[i], c[i], ss));
+            dot = fmaf(ta * wa[i], a[i], fmaf(tb * wb[i], c[i], dot));
+          }
+          ss = group_sum<kLanes>(ss);
+          dot = group_sum<kLanes>(dot);
+          // dx = r g w - x r^3 mean(g w x)
+          // (a group without a row adds nothing, whatever eps is)
+          const float r = h + u < end ? rsqrtf(fmaf(ss, 1.f / D, p.eps)) : 0.f;
+          const float back = dot * (1.f / D) * r * r * r;
+          float va[4], vb[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ga[i] *= r;
+            gb[i] *= r;
+            da[i] = fmaf(ga[i], a[i], da[i]);
+            db[i] = fmaf(gb[i], c[i], db[i]);
+            va[i] = fmaf(ga[i], wa[i], -a[i] * back);
+            vb[i] = fmaf(gb[i], wb[i], -c[i] * back);
+          }
+          if (h + u < end) store8<kHalves>(yrow + u * yh, lo, hi, va, vb);
+        }
+        yrow += kUnroll * yh;
       }
     }
   }
   if constexpr (kBwd) {
     // the block's sums, in a fixed order
-    __shared__ float part[kGroups][2][D];
+    __shared__ float part[kGroups][D];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = (i < 4 ? lo : hi) + (i & 3);
-      part[grp][0][c] = dw[0][i];
-      part[grp][1][c] = dw[1][i];
+    for (int i = 0; i < 4; ++i) {
+      part[grp][pair_col<kHalves>(lo, hi, i, 0)] = da[i];
+      part[grp][pair_col<kHalves>(lo, hi, i, 1)] = db[i];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kNrThreads) {
+    if (threadIdx.x < D) {
       float s = 0.f;
-      for (int g = 0; g < kGroups; ++g) s += part[g][0][i];
-      p.dw_part[(size_t)blockIdx.x * 2 * D + i] = s;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) s += part[g][threadIdx.x];
+      p.dw_part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * D + threadIdx.x] = s;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
 }
 
-// dw = sum over the blocks' partial rows, in a fixed order: one block for 32
-// columns, 8 warps over the rows, then over the warps.
-__global__ void __launch_bounds__(256)
-    tk_norm_rope_dw_kernel(const float *__restrict__ part, int rows, int D,
+// dw = sum over the blocks' partial rows, in a fixed order: a block for 32
+// columns of one weight, 32 warps over the rows, then over the warps.  Started
+// while the launch before ends.  grid: (D / 32, 2)
+__global__ void __launch_bounds__(1024)
+    tk_norm_rope_dw_kernel(const float *__restrict__ part, int q_rows, int k_rows, int D,
                            float *__restrict__ dqw, float *__restrict__ dkw) {
-  __shared__ float acc[8][32];
+  __shared__ float acc[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;  // of 2 D
-  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-  int r = warp;
-  for (; r + 24 < rows; r += 32) {
-    s0 += part[(size_t)r * 2 * D + col];
-    s1 += part[(size_t)(r + 8) * 2 * D + col];
-    s2 += part[(size_t)(r + 16) * 2 * D + col];
-    s3 += part[(size_t)(r + 24) * 2 * D + col];
+  const int col = blockIdx.x * 32 + lane;
+  const int rows = blockIdx.y ? k_rows : q_rows;
+  const float *base = part + (blockIdx.y ? (size_t)q_rows * D : 0) + col;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int r = warp; r < rows; r += 128) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r + 32 * i < rows) s[i] += base[(size_t)(r + 32 * i) * D];
   }
-  for (; r < rows; r += 8) s0 += part[(size_t)r * 2 * D + col];
-  acc[warp][lane] = (s0 + s1) + (s2 + s3);
+  acc[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
   if (warp == 0) {
-    float s = 0.f;
+    float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += acc[i][lane];
-    if (col < D)
-      dqw[col] = s;
-    else
-      dkw[col - D] = s;
+    for (int i = 0; i < 32; ++i) t += acc[i][lane];
+    (blockIdx.y ? dkw : dqw)[col] = t;
   }
 }
 
@@ -407,23 +439,24 @@ void fill(NrParams &p, const Call &c) {
   p.dw_part = nullptr;
 }
 
-// Heads a row group takes for one token: as many as keep every SM busy, up to
-// eight (the sines and cosines are then an eighth of a row's work).
-void split(NrParams &p, int D, int num_sms) {
+// Heads a row group takes for one token: fewer until there are blocks for
+// every SM (each run of heads computes the token's sines and cosines again), and
+// more again where the runs would pass the grid's second dimension.
+void split(NrParams &p, int D, int most, int max_runs, long long blocks_wanted) {
   const int groups = kNrThreads / (D / 8);
-  p.tiles = ((long long)p.B * p.N + groups - 1) / groups;
-  int hpg = 8;
-  while (hpg > 1 &&
-         p.tiles * ((p.H[0] + hpg - 1) / hpg + (p.H[1] + hpg - 1) / hpg) < 4LL * num_sms)
-    hpg /= 2;
+  p.tiles = (int)(((long long)p.B * p.N + groups - 1) / groups);
+  auto runs = [&](int hpg) {
+    return ((long long)p.H[0] + hpg - 1) / hpg + ((long long)p.H[1] + hpg - 1) / hpg;
+  };
+  int hpg = most;
+  while (hpg > 1 && p.tiles * runs(hpg) < blocks_wanted) hpg /= 2;
+  while (runs(hpg) > max_runs) hpg *= 2;
   p.hpg = hpg;
-  p.chunks[0] = (p.H[0] + hpg - 1) / hpg;
-  p.chunks[1] = (p.H[1] + hpg - 1) / hpg;
-  p.items = p.tiles * (p.chunks[0] + p.chunks[1]);
+  for (int i = 0; i < 2; ++i) p.chunks[i] = (p.H[i] + hpg - 1) / hpg;
 }
 
 template <bool kBwd>
-cudaError_t launch(const NrParams &p, int D, bool halves, int grid, cudaStream_t s) {
+cudaError_t launch(const NrParams &p, int D, bool halves, dim3 grid, cudaStream_t s) {
   if (D == 64) {
     if (halves)
       tk_norm_rope_kernel<64, true, kBwd><<<grid, kNrThreads, 0, s>>>(p);
@@ -488,8 +521,8 @@ extern "C" int tk_attn_qk_norm_rope(
     p.yb[i] = (long long)p.H[i] * N * D;
     p.dy[i] = {nullptr, 0, 0, 0};
   }
-  split(p, D, dv.num_sms);
-  const int grid = (int)(p.items < 0x7fffffffLL ? p.items : 0x7fffffffLL);
+  split(p, D, kNrFwdHeads, 65535, 4LL * dv.num_sms);
+  const dim3 grid(p.tiles, p.chunks[0] + p.chunks[1]);
   return launch<false>(p, D, !interleaved, grid, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? TK_ATTN_OK
@@ -497,7 +530,7 @@ extern "C" int tk_attn_qk_norm_rope(
 }
 
 extern "C" size_t tk_attn_qk_norm_rope_bwd_workspace_bytes(int D) {
-  return D == 64 || D == 128 ? (size_t)kNrBwdMaxBlocks * 2 * D * sizeof(float) : 0;
+  return D == 64 || D == 128 ? (size_t)kNrBwdMaxBlocks * D * sizeof(float) : 0;
 }
 
 extern "C" int tk_attn_qk_norm_rope_bwd_check_args(
@@ -584,12 +617,28 @@ extern "C" int tk_attn_qk_norm_rope_bwd(
              dq_out_strides[2]};
   p.dy[1] = {static_cast<const __nv_bfloat16 *>(dk_out), dk_out_strides[0], dk_out_strides[1],
              dk_out_strides[2]};
-  split(p, D, dv.num_sms);
+  // At most three blocks an SM (what is resident), each over several tiles.
+  split(p, D, kNrBwdHeads, kNrBwdMaxBlocks, 3LL * dv.num_sms);
   p.dw_part = static_cast<float *>(workspace);
-  const long long cap = 4LL * dv.num_sms < kNrBwdMaxBlocks ? 4LL * dv.num_sms : kNrBwdMaxBlocks;
-  const int grid = (int)(p.items < cap ? p.items : cap);
+  const int runs = p.chunks[0] + p.chunks[1];
+  int cols = 3 * dv.num_sms / runs;
+  cols = cols < 1 ? 1 : cols > p.tiles ? p.tiles : cols;
+  if ((long long)cols * runs > kNrBwdMaxBlocks) cols = kNrBwdMaxBlocks / runs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (launch<true>(p, D, !interleaved, grid, s) != cudaSuccess) return TK_ATTN_ERR_LAUNCH;
-  tk_norm_rope_dw_kernel<<<2 * D / 32, 256, 0, s>>>(p.dw_part, grid, D, dq_weight, dk_weight);
-  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+  if (launch<true>(p, D, !interleaved, dim3(cols, runs), s) != cudaSuccess)
+    return TK_ATTN_ERR_LAUNCH;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(D / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tk_norm_rope_dw_kernel,
+                            static_cast<const float *>(p.dw_part), cols * p.chunks[0],
+                            cols * p.chunks[1], D, dq_weight, dk_weight) == cudaSuccess
+             ? TK_ATTN_OK
+             : TK_ATTN_ERR_LAUNCH;
 }
