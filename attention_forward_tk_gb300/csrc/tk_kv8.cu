@@ -99,11 +99,10 @@ int log2i(int x) {
 
 // (a thread's registers hold its part of a whole page)
 template <int kPage>
-void launch_write(const Kv8WriteParams &p, int D, dim3 grid, cudaStream_t s) {
-  if (D == 64)
-    tk_kv8_write_kernel<64, kPage><<<grid, kKv8Threads, 0, s>>>(p);
-  else
-    tk_kv8_write_kernel<128, kPage><<<grid, kKv8Threads, 0, s>>>(p);
+cudaError_t launch_write(const Kv8WriteParams &p, int D, dim3 grid, cudaStream_t s) {
+  return launch_overlapped(
+      D == 64 ? tk_kv8_write_kernel<64, kPage> : tk_kv8_write_kernel<128, kPage>, grid,
+      kKv8Threads, 0, s, p);
 }
 
 size_t table_bytes(int B, int max_pages, int table_stride) {
@@ -178,13 +177,11 @@ extern "C" int tk_attn_kv8_write(const void *k, const long long *k_strides, cons
   p.err = dv.err_word;
   const dim3 grid(kv8_span(N, page), 2 * Hkv, B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  switch (page) {
-    case 16: launch_write<16>(p, D, grid, s); break;
-    case 32: launch_write<32>(p, D, grid, s); break;
-    case 64: launch_write<64>(p, D, grid, s); break;
-    default: launch_write<128>(p, D, grid, s); break;
-  }
-  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+  const cudaError_t e = page == 16   ? launch_write<16>(p, D, grid, s)
+                        : page == 32 ? launch_write<32>(p, D, grid, s)
+                        : page == 64 ? launch_write<64>(p, D, grid, s)
+                                     : launch_write<128>(p, D, grid, s);
+  return e == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }
 
 extern "C" int tk_attn_kv8_read_check_args(const void *k_cache, const void *v_cache,
@@ -237,11 +234,10 @@ extern "C" int tk_attn_kv8_read(const void *k_cache, const void *v_cache, const 
   p.err = dv.err_word;
   const dim3 grid((int)(((long long)N + 63) / 64), 2 * Hkv, B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 64)
-    tk_kv8_read_kernel<64><<<grid, kKv8Threads, 0, s>>>(p);
-  else
-    tk_kv8_read_kernel<128><<<grid, kKv8Threads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
+  const cudaError_t e =
+      launch_overlapped(D == 64 ? tk_kv8_read_kernel<64> : tk_kv8_read_kernel<128>, grid,
+                        kKv8Threads, 0, s, p);
+  return e == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }
 
 namespace tkattn {
@@ -269,30 +265,12 @@ size_t workspace_for(const DeviceView &dv, int B, int G, int Nq, int D) {
   return prefix_bytes(B) + (size_t)run_count(dv, G, Nq) * 2 * t * (D + 4) * sizeof(float);
 }
 
-// A merge that starts while the launch before still works, finds what it has
-// to do, and waits for it on the device.
-template <typename Kernel>
-cudaError_t launch_merge(Kernel kernel, dim3 grid, int threads, const Kv8AttnParams &p,
-                         cudaStream_t s) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <int D, int kNT>
 cudaError_t launch_decode(const Kv8AttnParams &p, cudaStream_t s) {
-  tk_kv8_decode_kernel<D, kNT><<<p.ctas, kDecThreads, DecCfg<D, kNT>::kSmem, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_overlapped(tk_kv8_decode_kernel<D, kNT>, p.ctas, kDecThreads,
+                                          DecCfg<D, kNT>::kSmem, s, p);
   if (e != cudaSuccess) return e;
-  return launch_merge(tk_kv8_merge_kernel<D>, dim3(p.g.Hkv, p.B, p.Nq * p.G), D, p,
-                      s);
+  return launch_overlapped(tk_kv8_merge_kernel<D>, dim3(p.g.Hkv, p.B, p.Nq * p.G), D, 0, s, p);
 }
 
 template <int D>
@@ -301,11 +279,12 @@ cudaError_t launch_chunk(const Kv8AttnParams &p, cudaStream_t s) {
   CUtensorMap tk, tv;
   if (!make_map_bytes(&tk, p.k, rows, D, p.g.page) || !make_map_bytes(&tv, p.v, rows, D, p.g.page))
     return cudaErrorInvalidValue;
-  tk_kv8_chunk_kernel<D><<<p.ctas, kChunkThreads, ChunkCfg<D>::kSmemAlloc, s>>>(tk, tv, p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_overlapped(tk_kv8_chunk_kernel<D>, p.ctas, kChunkThreads,
+                                          ChunkCfg<D>::kSmemAlloc, s, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_merge(tk_kv8_chunk_merge_kernel<D>,
-                      dim3((unsigned)(((long long)p.Nq * p.G + 7) / 8), p.g.Hkv, p.B), 256, p, s);
+  return launch_overlapped(tk_kv8_chunk_merge_kernel<D>,
+                           dim3((unsigned)(((long long)p.Nq * p.G + 7) / 8), p.g.Hkv, p.B), 256, 0,
+                           s, p);
 }
 
 }  // namespace

@@ -383,7 +383,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   volatile int *abort_flag = &sb.abort;
   const Kv8Geom &g = p.g;
 
-  grid_launch_dependents();
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sb.q_full[t], 4);
@@ -422,6 +421,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  grid_wait();
+  grid_launch_dependents();  // (after the wait: the merge reads the lengths before its own)
   if (blockIdx.x == 0) {  // report what is out of range, once
     bool bad = false;
 #pragma unroll 1
@@ -1031,6 +1032,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
     tk_kv8_chunk_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
   const int b = blockIdx.z, h = blockIdx.y;
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
   const ChunkSeq s = chunk_seq(p, b);
@@ -1048,7 +1050,7 @@ __global__ void __launch_bounds__(256)
     before += __shfl_xor_sync(0xffffffffu, before, d);
     all += __shfl_xor_sync(0xffffffffu, all, d);
   }
-  grid_wait();  // every block waits: this launch's end means the end of the one before too
+  grid_wait();  // (above: only what the launch before leaves alone)
   if (r >= s.rows * p.G) return;
   const long long share = p.prefix[p.B];
   const long long s0 = p.prefix[b] + h * all + before;

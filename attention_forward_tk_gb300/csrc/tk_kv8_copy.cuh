@@ -23,6 +23,7 @@
 #include "sm103_ptx.cuh"
 #include "tk_device.h"
 #include "tk_kv8.h"
+#include "tk_launch.cuh"
 
 namespace tkattn {
 
@@ -108,6 +109,8 @@ __global__ void __launch_bounds__(kKv8Threads)
   const int b = blockIdx.z;
   const int which = blockIdx.y >= g.Hkv;
   const int h = blockIdx.y - (which ? g.Hkv : 0);
+  grid_launch_dependents();
+  grid_wait();
   bool bad = false;
   const int start = p.start[b];
   const int n = kv8_write_rows(g, start, p.counts ? p.counts[b] : p.N, p.N, &bad);
@@ -215,6 +218,8 @@ __global__ void __launch_bounds__(kKv8Threads)
   const int b = blockIdx.z;
   const int which = blockIdx.y >= g.Hkv;
   const int h = blockIdx.y - (which ? g.Hkv : 0);
+  grid_launch_dependents();
+  grid_wait();
   bool bad = false;
   const int len = kv8_length(g, p.lengths[b], &bad);
   if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)

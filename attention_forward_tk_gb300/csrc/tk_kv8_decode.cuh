@@ -55,6 +55,7 @@
 #include "tk_device.h"
 #include "tk_kv8.h"
 #include "tk_kv8_copy.cuh"
+#include "tk_launch.cuh"
 
 namespace tkattn {
 
@@ -231,15 +232,6 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t &a, uint3
       : "r"(w));
 }
 
-// This launch's dependents may start (they wait before they read); and wait
-// for the launch this one depends on.
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void grid_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Any byte of w an E4M3 NaN (0x7f or 0xff).
 __device__ __forceinline__ bool has_nan4(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
@@ -282,7 +274,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   float *merge_o = reinterpret_cast<float *>(smem + C::kRingBytes);
   float *merge_s = merge_o + kDecWarps * C::kRows * C::kRowStride;  // m, M, l of each warp's rows
 
-  grid_launch_dependents();
+  grid_wait();
+  grid_launch_dependents();  // (after the wait: the merge reads the lengths before its own)
   if (blockIdx.x == 0) {  // report what is out of range, once
     bool bad = false;
 #pragma unroll 1
@@ -726,6 +719,8 @@ __global__ void __launch_bounds__(D)
     tk_kv8_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
   __shared__ Kv8Place place;
   __shared__ long long red[4];
+  // (It does not let its dependents begin: the next call's runs, resident early,
+  // would take the registers that these blocks need; 161 -> 228 us at 8 x 16384.)
   const int h = blockIdx.x, b = blockIdx.y, r = blockIdx.z;
   const int segs = p.g.Hkv;
   bool bad = false;
@@ -737,8 +732,8 @@ __global__ void __launch_bounds__(D)
   const long long share = place.share;
   const long long s0 = place.prefix + (long long)h * units;
   const int c0 = (int)(s0 / share), c1 = (int)((s0 + max(units, 1) - 1) / share);
-  // All above reads only what the launch before leaves alone.  Every block
-  // waits, so that this launch's end means the end of the one before too.
+  // All above reads only what the launch before leaves alone, and what came
+  // before that one has ended (it starts this one after its own wait).
   grid_wait();
   if (r >= rows * p.G || c0 == c1) return;
   // run c0's partial is its first segment's only if it starts where the segment does

@@ -31,6 +31,7 @@
 #include "sm103_ptx.cuh"
 #include "tk_attn.h"
 #include "tk_device.h"
+#include "tk_launch.cuh"
 
 namespace tkattn {
 namespace {
@@ -169,6 +170,8 @@ __global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4)
   const int which = (int)blockIdx.y >= p.chunks[0];
   const int h0 = ((int)blockIdx.y - (which ? p.chunks[0] : 0)) * p.hpg;
   const int h1 = min(h0 + p.hpg, p.H[which]);
+  grid_launch_dependents();
+  grid_wait();
   const NrTensor X = p.x[which];
   const long long yh = p.yh[which];
   float wa[4], wb[4];
@@ -297,7 +300,6 @@ __global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4)
       for (int g = 0; g < kGroups; ++g) s += part[g][threadIdx.x];
       p.dw_part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * D + threadIdx.x] = s;
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
 }
 
@@ -312,7 +314,8 @@ __global__ void __launch_bounds__(1024)
   const int col = blockIdx.x * 32 + lane;
   const int rows = blockIdx.y ? k_rows : q_rows;
   const float *base = part + (blockIdx.y ? (size_t)q_rows * D : 0) + col;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_launch_dependents();
+  grid_wait();
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   for (int r = warp; r < rows; r += 128) {
 #pragma unroll
@@ -457,18 +460,11 @@ void split(NrParams &p, int D, int most, int max_runs, long long blocks_wanted) 
 
 template <bool kBwd>
 cudaError_t launch(const NrParams &p, int D, bool halves, dim3 grid, cudaStream_t s) {
-  if (D == 64) {
-    if (halves)
-      tk_norm_rope_kernel<64, true, kBwd><<<grid, kNrThreads, 0, s>>>(p);
-    else
-      tk_norm_rope_kernel<64, false, kBwd><<<grid, kNrThreads, 0, s>>>(p);
-  } else {
-    if (halves)
-      tk_norm_rope_kernel<128, true, kBwd><<<grid, kNrThreads, 0, s>>>(p);
-    else
-      tk_norm_rope_kernel<128, false, kBwd><<<grid, kNrThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  const auto kernel = D == 64 ? (halves ? tk_norm_rope_kernel<64, true, kBwd>
+                                        : tk_norm_rope_kernel<64, false, kBwd>)
+                              : (halves ? tk_norm_rope_kernel<128, true, kBwd>
+                                        : tk_norm_rope_kernel<128, false, kBwd>);
+  return launch_overlapped(kernel, grid, kNrThreads, 0, s, p);
 }
 
 }  // namespace
@@ -627,18 +623,9 @@ extern "C" int tk_attn_qk_norm_rope_bwd(
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch<true>(p, D, !interleaved, dim3(cols, runs), s) != cudaSuccess)
     return TK_ATTN_ERR_LAUNCH;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(D / 32, 2);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tk_norm_rope_dw_kernel,
-                            static_cast<const float *>(p.dw_part), cols * p.chunks[0],
-                            cols * p.chunks[1], D, dq_weight, dk_weight) == cudaSuccess
+  return launch_overlapped(tk_norm_rope_dw_kernel, dim3(D / 32, 2), 1024, 0, s, p.dw_part,
+                           cols * p.chunks[0], cols * p.chunks[1], D, dq_weight,
+                           dk_weight) == cudaSuccess
              ? TK_ATTN_OK
              : TK_ATTN_ERR_LAUNCH;
 }

@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -84,7 +84,7 @@ tk_attn_stream_t stream_of(int dev) {
 }
 
 Tensor make(Shape shape, at::ScalarType dtype, const Tensor &like) {
-  return at::empty(shape, like.options().dtype(dtype).requires_grad(false));
+  return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
 }
 
 // What the C calls take of each argument.
