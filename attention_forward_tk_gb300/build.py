@@ -79,7 +79,7 @@ def build_binding(force: bool = False) -> str:
            "-I", INCLUDE, "-I", cuda, "-I", sysconfig.get_paths()["include"],
            "-isystem", headers, "-isystem", os.path.join(headers, "torch", "csrc", "api", "include"),
            BINDING_SOURCE, "-o", tmp, "-L", BUILD_DIR, "-l:libtk_attn.so", "-L",
-           os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -270,7 +270,8 @@ cudaError_t launch_decode(const Kv8AttnParams &p, cudaStream_t s) {
   const cudaError_t e = launch_overlapped(tk_kv8_decode_kernel<D, kNT>, p.ctas, kDecThreads,
                                           DecCfg<D, kNT>::kSmem, s, p);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(tk_kv8_merge_kernel<D>, dim3(p.g.Hkv, p.B, p.Nq * p.G), D, 0, s, p);
+  return launch_overlapped(tk_kv8_merge_kernel<D>, dim3(p.g.Hkv, p.B, p.Nq * p.G),
+                           kMergeWarps * 32, 0, s, p);
 }
 
 template <int D>
@@ -318,6 +319,9 @@ extern "C" int tk_attn_fwd_kv8_check_args(const void *q, const void *k_cache, co
   if (B > 65535 || Nq * G * G > 0x7fffffffLL ||
       (long long)Hkv * (((long long)Nq * G + 7) / 8) > 0x7fffffffLL ||
       (long long)B * H > 0x7fffffffLL)
+    return TK_ATTN_ERR_UNSUPPORTED;
+  // few rows count units of 64 positions in 32 bits (with room for a share)
+  if ((long long)B * Hkv * ((long long)max_pages * page / 64 + 1) > (1LL << 30))
     return TK_ATTN_ERR_UNSUPPORTED;
   const size_t payload = (size_t)num_pages * Hkv * page * D, exps = (size_t)num_pages * Hkv;
   const size_t dense = (size_t)B * H * Nq * D * 2;

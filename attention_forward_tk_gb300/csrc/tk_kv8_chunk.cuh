@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (bad) atomicCAS(p.err, 0, kDevErrIndex);
   }
   kv8_scan(
-      p, [&](int b) { return chunk_seq_cost(p, b) * p.g.Hkv; }, blockIdx.x, -1, &sb.place, sb.red,
+      p, [&](int b) { return chunk_seq_cost(p, b) * p.g.Hkv; }, blockIdx.x, &sb.place, sb.red,
       blockIdx.x == 0 ? p.prefix : nullptr);
   tc_fence_before_sync();
   __syncthreads();

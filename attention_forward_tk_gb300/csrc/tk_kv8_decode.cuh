@@ -137,12 +137,11 @@ struct Kv8Place {
 };
 
 // Total work (cost(b) over the sequences), and the sequence in which run `run`
-// starts (b = B when past the end), or with find_b >= 0 the work before
-// sequence find_b.  With `prefix` the work before each sequence is written
+// starts (b = B when past the end).  With `prefix` the work before each sequence is written
 // there, a run's share last.  Whole block; ends with a barrier.
 template <typename Cost>
-__device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, Cost cost, int run, int find_b,
-                                         Kv8Place *out, long long *red, long long *prefix) {
+__device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, Cost cost, int run, Kv8Place *out,
+                                         long long *red, long long *prefix) {
   const int nthr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long v0 = (int)threadIdx.x < p.B ? cost(threadIdx.x) : 0;
   long long sum = v0;
@@ -187,13 +186,83 @@ __device__ __forceinline__ void kv8_scan(const Kv8AttnParams &p, Cost cost, int 
     const long long lo = before + inc - v;
     if (b < p.B) {
       if (prefix) prefix[b] = lo;
-      if (find_b >= 0 ? b == find_b : (u >= lo && u < lo + v)) {
+      if (u >= lo && u < lo + v) {
         out->b = b;
         out->prefix = lo;
       }
     }
     __syncthreads();
   }
+}
+
+// The same for few rows, in 32 bits (the host bounds the units) and with one
+// value a thread in hand: total work, and where run `run` starts.  Two barriers
+// for up to kDecThreads sequences.
+struct DecPlace {
+  int total, share, b, prefix;
+};
+__device__ __forceinline__ void dec_scan(const Kv8AttnParams &p, int run, DecPlace *out,
+                                         int (*red)[kDecWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int v0 = (int)threadIdx.x < p.B ? seq_units(p, threadIdx.x, kDecUnit) * p.g.Hkv : 0;
+  int sum = v0, inc = v0;
+#pragma unroll 1
+  for (int b = threadIdx.x + kDecThreads; b < p.B; b += kDecThreads)
+    sum += seq_units(p, b, kDecUnit) * p.g.Hkv;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += t;
+  }
+  if (lane == 31) {
+    red[0][warp] = sum;
+    red[1][warp] = inc;
+  }
+  __syncthreads();
+  int total = 0, lo = inc - v0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    total += red[0][w];
+    if (w < warp) lo += red[1][w];
+    all += red[1][w];
+  }
+  const int share = max(1, (int)(((unsigned)total + p.ctas - 1) / (unsigned)p.ctas));
+  const int u = run * share;  // (at most the total and a share)
+  if (threadIdx.x == 0) {
+    out->total = total;
+    out->share = share;
+  }
+  if (u >= lo && u < lo + v0) {
+    out->b = threadIdx.x;
+    out->prefix = lo;
+  }
+#pragma unroll 1
+  for (int base = kDecThreads; base < p.B && all <= u; base += kDecThreads) {
+    // more sequences than threads: on to the next kDecThreads of them
+    const int b = base + threadIdx.x;
+    const int v = b < p.B ? seq_units(p, b, kDecUnit) * p.g.Hkv : 0;
+    inc = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += t;
+    }
+    __syncthreads();
+    if (lane == 31) red[1][warp] = inc;
+    __syncthreads();
+    lo = all + inc - v;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (w < warp) lo += red[1][w];
+      all += red[1][w];
+    }
+    if (u >= lo && u < lo + v) {
+      out->b = b;
+      out->prefix = lo;
+    }
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -265,8 +334,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   constexpr int kChunks = D / 64;  // 16-byte pieces of a key row a lane takes
   constexpr int kVw = D / 32;      // words of a value row a lane takes
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Kv8Place place;
-  __shared__ long long red[kDecWarps];
+  __shared__ DecPlace place;
+  __shared__ int red[2][kDecWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q8 = lane >> 2, c4 = lane & 3;
   const Kv8Geom &g = p.g;
@@ -285,13 +354,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     }
     if (bad) atomicCAS(p.err, 0, kDevErrIndex);
   }
-  kv8_scan(
-      p, [&](int b) { return (long long)seq_units(p, b, kDecUnit) * segs; }, blockIdx.x, -1,
-      &place, red, nullptr);
-  const long long share = place.share;
-  const long long u0 = blockIdx.x * share;
+  dec_scan(p, blockIdx.x, &place, red);
+  const int u0 = blockIdx.x * place.share;
   if (u0 >= place.total) return;
-  const int nsteps = (int)min(share, place.total - u0);
+  const int nsteps = min(place.share, place.total - u0);
 
   DecCursor cons;
   {
@@ -299,9 +365,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     cons.b = place.b;
     cons.units = seq_units(p, cons.b, kDecUnit);
     cons.len = seq_len(p, cons.b, &bad);
-    const long long l = u0 - place.prefix;
-    cons.seg = (int)(l / cons.units);
-    cons.unit = (int)(l % cons.units);
+    cons.seg = (u0 - place.prefix) / cons.units;
+    cons.unit = u0 - place.prefix - cons.seg * cons.units;
   }
   DecCursor prod = cons;
 
@@ -711,49 +776,119 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   }
 }
 
-// Merge of the runs' partial results: one block (a thread a column) for each
-// (head, sequence, row).  Segments that one run held whole are
-// already written.
+// Merge of the runs' partial results: a block for each (head, sequence, row).
+// A warp takes every eighth partial, its lanes D/32 columns each; then the warps
+// are joined.  Segments that one run held whole are already written.
+constexpr int kMergeWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(kMergeWarps * 32)
     tk_kv8_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
-  __shared__ Kv8Place place;
-  __shared__ long long red[4];
+  constexpr int kPer = D / 32;
+  __shared__ int red[2][kMergeWarps];
+  __shared__ float stat[kMergeWarps][3];
+  __shared__ float cols[kMergeWarps][D];
   // (It does not let its dependents begin: the next call's runs, resident early,
   // would take the registers that these blocks need; 161 -> 228 us at 8 x 16384.)
   const int h = blockIdx.x, b = blockIdx.y, r = blockIdx.z;
-  const int segs = p.g.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool bad = false;
   const int rows = seq_rows(p, b, &bad);
-  kv8_scan(
-      p, [&](int b) { return (long long)seq_units(p, b, kDecUnit) * segs; }, 0, b, &place, red,
-      nullptr);
+  // the units before this sequence, and all of them
+  int before = 0, total = 0;
+#pragma unroll 1
+  for (int x = threadIdx.x; x < p.B; x += kMergeWarps * 32) {
+    const int v = seq_units(p, x, kDecUnit) * p.g.Hkv;
+    total += v;
+    if (x < b) before += v;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) {
+    red[0][warp] = before;
+    red[1][warp] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    before += red[0][w];
+    total += red[1][w];
+  }
   const int units = seq_units(p, b, kDecUnit);
-  const long long share = place.share;
-  const long long s0 = place.prefix + (long long)h * units;
-  const int c0 = (int)(s0 / share), c1 = (int)((s0 + max(units, 1) - 1) / share);
+  const int share = max(1, (int)(((unsigned)total + p.ctas - 1) / (unsigned)p.ctas));
+  const int s0 = before + h * units;
+  const int c0 = s0 / share, c1 = (s0 + max(units, 1) - 1) / share;
+  // run c0's partial is its first segment's only if it starts where the segment does
+  const int first0 = c0 * share == s0 ? 0 : 1;
+  const float *base = p.part + (size_t)r * (D + 4);
+  const size_t slot = (size_t)p.tile_rows * (D + 4);
   // All above reads only what the launch before leaves alone, and what came
   // before that one has ended (it starts this one after its own wait).
   grid_wait();
   if (r >= rows * p.G || c0 == c1) return;
-  // run c0's partial is its first segment's only if it starts where the segment does
-  const float *base = p.part + (size_t)r * (D + 4);
-  const size_t slot = (size_t)p.tile_rows * (D + 4);
-  const int first0 = c0 * share == s0 ? 0 : 1;
-  auto at = [&](int c) { return base + ((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot; };
-  float mm = kDecNone, mmo = kDecNone;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    mm = fmaxf(mm, at(c)[D]);
-    mmo = fmaxf(mmo, at(c)[D + 1]);
+  float mm = kDecNone, mmo = kDecNone, ll = 0.f, acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+  constexpr int kDeep = 4;  // partials in flight
+#pragma unroll 1
+  for (int c = c0 + warp; c <= c1; c += kMergeWarps * kDeep) {
+    float4 st[kDeep];
+    float x[kDeep][kPer];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int ci = c + i * kMergeWarps;
+      st[i] = make_float4(kDecNone, kDecNone, 0.f, 0.f);
+      if (ci <= c1) {
+        const float *d = base + ((size_t)ci * 2 + (ci == c0 ? first0 : 0)) * slot;
+        st[i] = *reinterpret_cast<const float4 *>(d + D);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) x[i][k] = d[lane * kPer + k];
+      }
+    }
+    float m_new = mm, mo_new = mmo;
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      m_new = fmaxf(m_new, st[i].x);
+      mo_new = fmaxf(mo_new, st[i].y);
+    }
+    ll *= ex2_approx(mm - m_new);
+    const float up = ex2_approx(mmo - mo_new);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] *= up;
+    mm = m_new;
+    mmo = mo_new;
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      // nothing seen: l is 0 (a NaN score leaves l NaN, which has to stay)
+      if (st[i].z == 0.f) continue;
+      ll += st[i].z * ex2_approx(st[i].x - mm);
+      const float wt = ex2_approx(st[i].y - mmo);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(wt, x[i][k], acc[k]);
+    }
   }
-  float ll = 0.f, out = 0.f;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const float *d = at(c);
-    const float l = d[D + 2];
-    ll += l == 0.f ? 0.f : l * ex2_approx(d[D] - mm);
-    out = fmaf(l == 0.f ? 0.f : ex2_approx(d[D + 1] - mmo), d[threadIdx.x], out);
+  if (lane == 0) {
+    stat[warp][0] = mm;
+    stat[warp][1] = mmo;
+    stat[warp][2] = ll;
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) cols[warp][lane * kPer + k] = acc[k];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  mm = mmo = kDecNone;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    mm = fmaxf(mm, stat[w][0]);
+    mmo = fmaxf(mmo, stat[w][1]);
+  }
+  ll = 0.f;
+  float out = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    if (stat[w][2] == 0.f) continue;
+    ll += stat[w][2] * ex2_approx(stat[w][0] - mm);
+    out = fmaf(ex2_approx(stat[w][1] - mmo), cols[w][threadIdx.x], out);
   }
   const int i = row_query(p, r);
   const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
