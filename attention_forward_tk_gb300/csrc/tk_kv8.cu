@@ -284,7 +284,7 @@ cudaError_t launch_chunk(const Kv8AttnParams &p, cudaStream_t s) {
                                           ChunkCfg<D>::kSmemAlloc, s, tk, tv, p);
   if (e != cudaSuccess) return e;
   return launch_overlapped(tk_kv8_chunk_merge_kernel<D>,
-                           dim3((unsigned)(((long long)p.Nq * p.G + 7) / 8), p.g.Hkv, p.B), 256, 0,
+                           dim3((unsigned)(((long long)p.Nq * p.G + 31) / 32), p.g.Hkv, p.B), 256, 0,
                            s, p);
 }
 

@@ -144,15 +144,26 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const Kv8AttnParams &p, int b) {
   s.units = (s.rows * p.G + kChunkRows - 1) / kChunkRows;
   return s;
 }
+// Key tiles of unit mb: those of its last row.
 __device__ __forceinline__ int chunk_cost(const Kv8AttnParams &p, const ChunkSeq &s, int mb) {
-  return max(chunk_tiles(p, mb * kChunkRows, s.len, s.rows),
-             chunk_tiles(p, mb * kChunkRows + 128, s.len, s.rows));
+  const int last = min(mb * kChunkRows + kChunkRows, s.rows * p.G) - 1;
+  return max(1, (row_sees(p, row_query(p, last), s.len, s.rows) + 127) / 128);
 }
+// A head's units together: by one thread, or by a warp.
 __device__ __forceinline__ long long chunk_seq_cost(const Kv8AttnParams &p, int b) {
   const ChunkSeq s = chunk_seq(p, b);
   long long c = 0;
 #pragma unroll 1
   for (int mb = 0; mb < s.units; ++mb) c += chunk_cost(p, s, mb);
+  return c;
+}
+__device__ __forceinline__ long long chunk_seq_cost_warp(const Kv8AttnParams &p, int b, int lane) {
+  const ChunkSeq s = chunk_seq(p, b);
+  long long c = 0;
+#pragma unroll 1
+  for (int mb = lane; mb < s.units; mb += 32) c += chunk_cost(p, s, mb);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
   return c;
 }
 
@@ -197,23 +208,30 @@ __device__ __forceinline__ float chunk_queries(const Kv8AttnParams &p, int b, in
   constexpr int kLanes = D / 8;           // lanes of a row, 8 values each
   constexpr int kPerIt = 32 / kLanes;     // rows a pass
   constexpr int kIts = 32 / kPerIt;
+  constexpr int kDeep = 4;                // passes loaded together, one batch ahead
   const int l = lane % kLanes, sub = lane / kLanes;
   float mine = 1.f;
-#pragma unroll 1
-  for (int it0 = 0; it0 < kIts; it0 += 2) {
-    if (first + w * 32 + it0 * kPerIt >= r_end) break;  // no row left (warp-uniform)
-    uint4 v[2];
+  auto load = [&](int it) -> uint4 {
+    const int r = first + w * 32 + it * kPerIt + sub;
+    if (r >= r_end) return make_uint4(0, 0, 0, 0);
+    const int i = row_query(p, r);
+    return *reinterpret_cast<const uint4 *>(
+        p.q + (((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i) * D + l * 8);
+  };
+  uint4 ahead[kDeep];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = first + w * 32 + (it0 + u) * kPerIt + sub;
-      const int i = row_query(p, r);
-      v[u] = r < r_end ? *reinterpret_cast<const uint4 *>(
-                             p.q + (((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i) * D +
-                             l * 8)
-                       : make_uint4(0, 0, 0, 0);
+  for (int u = 0; u < kDeep; ++u) ahead[u] = load(u);
+#pragma unroll 1
+  for (int it0 = 0; it0 < kIts; it0 += kDeep) {
+    if (first + w * 32 + it0 * kPerIt >= r_end) break;  // no row left (warp-uniform)
+    uint4 v[kDeep];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      v[u] = ahead[u];
+      ahead[u] = it0 + kDeep < kIts ? load(it0 + kDeep + u) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kDeep; ++u) {
       const int row = w * 32 + (it0 + u) * kPerIt + sub;  // row of the tile
       const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
       uint32_t am = 0;
@@ -432,9 +450,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     if (bad) atomicCAS(p.err, 0, kDevErrIndex);
   }
+  // The work of each sequence.  Where sequences have many units (the lower
+  // bound by the call's sizes) a warp sums one, into shared memory that the
+  // rings use later; else, or where those sums would not fit, a thread does.
+  long long *sums = reinterpret_cast<long long *>(smem);
+  const bool by_warp = p.Nq * p.G > 8 * kChunkRows && p.B <= C::kSmem / 8;
+  if (by_warp) {
+#pragma unroll 1
+    for (int b = warp; b < p.B; b += kChunkThreads / 32) {
+      const long long c = chunk_seq_cost_warp(p, b, lane);
+      if (lane == 0) sums[b] = c;
+    }
+    __syncthreads();
+  }
   kv8_scan(
-      p, [&](int b) { return chunk_seq_cost(p, b) * p.g.Hkv; }, blockIdx.x, &sb.place, sb.red,
-      blockIdx.x == 0 ? p.prefix : nullptr);
+      p, [&](int b) { return (by_warp ? sums[b] : chunk_seq_cost(p, b)) * p.g.Hkv; }, blockIdx.x,
+      &sb.place, sb.red, blockIdx.x == 0 ? p.prefix : nullptr);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -950,7 +981,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_wait(&sb.mma_done, 0, &never);
       }
     }
-    if (warp == 15 && lane == 0) {
+    if (warp == 15) {
       // ---------------------------------------------------------- the run's segments
       const long long share = sb.place.share;
       const long long u0 = blockIdx.x * share;
@@ -958,17 +989,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       int b = sb.place.b, h = 0, mb = 0, j = 0;
       ChunkSeq q = {0, 0, 0};
       if (left > 0) {
+        // where the run starts: the head, then the unit, 32 units at a time
         q = chunk_seq(p, b);
+        const long long per_head = chunk_seq_cost_warp(p, b, lane);
         long long r = u0 - sb.place.prefix;
-        const long long per_head = chunk_seq_cost(p, b);
         h = (int)(r / per_head);
         r -= h * per_head;
 #pragma unroll 1
-        for (int c; r >= (c = chunk_cost(p, q, mb)); ++mb) r -= c;
-        j = (int)r;
+        for (int m0 = 0;; m0 += 32) {
+          const int c = m0 + lane < q.units ? chunk_cost(p, q, m0 + lane) : 0;
+          int inc = c;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += t;
+          }
+          const uint32_t in = __ballot_sync(0xffffffffu, r < inc);
+          if (in != 0 || m0 + 32 >= q.units) {
+            const int at = in != 0 ? __ffs(in) - 1 : 31;  // (always found)
+            mb = m0 + at;
+            j = (int)(r - __shfl_sync(0xffffffffu, inc - c, at));
+            break;
+          }
+          r -= __shfl_sync(0xffffffffu, inc, 31);
+        }
       }
+      if (lane != 0) left = 0;  // one thread posts them
 #pragma unroll 1
-      for (uint32_t x = 0;; ++x) {
+      for (uint32_t x = 0; lane == 0; ++x) {
         if (x >= 4 && !mbar_wait(&sb.seg_empty[x & 3], ((x >> 2) - 1) & 1, abort_flag)) {
           chunk_abort(sb, p.err);
           break;
@@ -1026,18 +1074,20 @@ done:
   }
 }
 
-// Merge of the runs' partial results (O / l and LSE of a run): a warp a row,
-// eight rows a block.  grid: (ceil(Nq * G / 8), Hkv, B)
+// Merge of the runs' partial results (O / l and LSE of a run): a warp takes four
+// rows of one tile, all their partials of a run in flight together.
+// grid: (ceil(Nq * G / 32), Hkv, B)
+constexpr int kChunkMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
     tk_kv8_chunk_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
+  constexpr int kPer = D / 32;
   const int b = blockIdx.z, h = blockIdx.y;
-  grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int r0 = blockIdx.x * (8 * kChunkMergeRows) + (threadIdx.x >> 5) * kChunkMergeRows;
   const ChunkSeq s = chunk_seq(p, b);
-  const int mb = r / kChunkRows;
-  // steps of the head's units before this row's, and of all of them
+  const int mb = r0 / kChunkRows, r_end = s.rows * p.G;
+  // steps of the head's units before these rows', and of all of them
   long long before = 0, all = 0;
 #pragma unroll 1
   for (int x = lane; x < s.units; x += 32) {
@@ -1051,44 +1101,64 @@ __global__ void __launch_bounds__(256)
     all += __shfl_xor_sync(0xffffffffu, all, d);
   }
   grid_wait();  // (above: only what the launch before leaves alone)
-  if (r >= s.rows * p.G) return;
+  if (r0 >= r_end) return;
   const long long share = p.prefix[p.B];
   const long long s0 = p.prefix[b] + h * all + before;
   const int cost = chunk_cost(p, s, mb);
   const int c0 = (int)(s0 / share), c1 = (int)((s0 + cost - 1) / share);
   if (c0 == c1) return;
-  const int t = (r / 128) & 1;
-  const int tiles = chunk_tiles(p, mb * kChunkRows + t * 128, s.len, s.rows);
-  const size_t slot = (size_t)kChunkRows * (D + 4);
-  const float *base = p.part + (size_t)(r % kChunkRows) * (D + 4);
-  const int first0 = c0 * share == s0 ? 0 : 1;
-  constexpr int kPer = D / 32;
-  // runs that hold no key tile of this row's tile wrote nothing for it
+  // runs that hold no key tile of these rows' tile wrote nothing for them
+  const int tiles = chunk_tiles(p, r0 / 128 * 128, s.len, s.rows);
   const int c_end = min(c1, (int)((s0 + tiles - 1) / share));
-  float mx = -INFINITY;
-  for (int c = c0; c <= c_end; ++c)
-    mx = fmaxf(mx, base[((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot + D]);
-  const float mu = mx == -INFINITY ? 0.f : mx;
-  float z = 0.f, acc[kPer];
+  const size_t slot = (size_t)kChunkRows * (D + 4);
+  const float *base = p.part + (size_t)(r0 % kChunkRows) * (D + 4);
+  const int first0 = c0 * share == s0 ? 0 : 1;
+  float mx[kChunkMergeRows], z[kChunkMergeRows], acc[kChunkMergeRows][kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+  for (int i = 0; i < kChunkMergeRows; ++i) {
+    mx[i] = kDecNone;
+    z[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[i][k] = 0.f;
+  }
+#pragma unroll 2
   for (int c = c0; c <= c_end; ++c) {
     const float *d = base + ((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot;
-    const float w = expf(d[D] - mu);
-    z += w;
+    float l[kChunkMergeRows], x[kChunkMergeRows][kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, d[lane * kPer + i], acc[i]);
+    for (int i = 0; i < kChunkMergeRows; ++i) {
+      l[i] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) x[i][k] = 0.f;
+      if (r0 + i < r_end) {
+        l[i] = d[i * (D + 4) + D];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) x[i][k] = d[i * (D + 4) + lane * kPer + k];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kChunkMergeRows; ++i) {
+      const float m = fmaxf(mx[i], l[i]);
+      const float up = expf(mx[i] - m), w = expf(l[i] - m);  // (l -inf: 0; NaN stays)
+      mx[i] = m;
+      z[i] = fmaf(z[i], up, w);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[i][k] = fmaf(w, x[i][k], acc[i][k] * up);
+    }
   }
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  const int i = row_query(p, r);
-  const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
-  uint32_t pk[kPer / 2];
 #pragma unroll
-  for (int k = 0; k < kPer / 2; ++k) pk[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * kPer);
+  for (int i = 0; i < kChunkMergeRows; ++i) {
+    const int r = r0 + i;
+    if (r >= r_end) break;
+    const float inv = z[i] == 0.f ? 0.f : 1.f / z[i];
+    const int n = row_query(p, r);
+    const long long orow = ((long long)b * p.H + h * p.G + (r - n * p.G)) * p.Nq + n;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * kPer);
 #pragma unroll
-  for (int k = 0; k < kPer / 2; ++k) dst[k] = pk[k];
-  if (lane == 0) p.lse[orow] = z == 0.f ? -INFINITY : mu + logf(z);
+    for (int k = 0; k < kPer / 2; ++k)
+      dst[k] = pack_bf16x2(acc[i][2 * k] * inv, acc[i][2 * k + 1] * inv);
+    if (lane == 0) p.lse[orow] = z[i] == 0.f ? -INFINITY : mx[i] + logf(z[i]);
+  }
 }
 
 }  // namespace tkattn
