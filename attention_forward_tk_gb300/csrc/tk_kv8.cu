@@ -47,8 +47,10 @@ int kv8_device(DeviceView *dv) {
   if (st) return st;
   Kv8Device &d = g_kv8_dev[dv->index];
   std::call_once(d.once, [&d] {
-    d.ok = configure_decode<64, 1>() && configure_decode<64, 2>() && configure_decode<128, 1>() &&
-           configure_decode<128, 2>() && configure_chunk<64>() && configure_chunk<128>();
+    d.ok = configure_decode<64, 1>() && configure_decode<64, 2>() && configure_decode<64, 3>() &&
+           configure_decode<64, 5>() && configure_decode<128, 1>() && configure_decode<128, 2>() &&
+           configure_decode<128, 3>() &&
+           configure_chunk<64>() && configure_chunk<128>();
   });
   return d.ok ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }
@@ -243,15 +245,23 @@ extern "C" int tk_attn_kv8_read(const void *k_cache, const void *v_cache, const 
 namespace tkattn {
 namespace {
 
-// At most 16 query rows a (sequence, key/value head) stream the cache past
-// 8-row or 16-row tiles; more go to the 128-row tiles of the tensor core.
-bool few_rows(int G, int Nq) { return (long long)Nq * G <= 16; }
-int tile_rows(int G, int Nq) { return (long long)Nq * G <= 8 ? 8 : 16; }
+// Tiles of eight query rows that a warp of the streaming kernel holds for a
+// call's Nq * G rows, or 0 where the rows go to the 128-row tiles of the tensor
+// core: past 24 rows at D = 128 and 40 at D = 64 the registers spill.
+int row_tiles(int G, int Nq, int D) {
+  const long long tiles = ((long long)Nq * G + 7) / 8;
+  if (tiles <= 3) return (int)tiles;
+  return D == 64 && tiles <= 5 ? 5 : 0;
+}
 // Runs the work is cut into: the CTAs that fit on the device at once.
-int run_count(const DeviceView &dv, int G, int Nq) {
-  if (!few_rows(G, Nq)) return dv.num_sms;
-  return (tile_rows(G, Nq) == 8 ? DecCfg<128, 1>::kCtasPerSm : DecCfg<128, 2>::kCtasPerSm) *
-         dv.num_sms;
+int run_count(const DeviceView &dv, int tiles, int D) {
+  if (tiles == 0) return dv.num_sms;
+  const int per_sm = D == 64 ? (tiles <= 1   ? DecCfg<64, 1>::kCtasPerSm
+                               : tiles <= 3 ? DecCfg<64, 3>::kCtasPerSm
+                                            : DecCfg<64, 5>::kCtasPerSm)
+                             : (tiles == 1 ? DecCfg<128, 1>::kCtasPerSm
+                                           : DecCfg<128, 3>::kCtasPerSm);
+  return per_sm * dv.num_sms;
 }
 
 bool sizes_ok(int B, int H, int Hkv, int Nq, int D) {
@@ -261,8 +271,9 @@ bool sizes_ok(int B, int H, int Hkv, int Nq, int D) {
 size_t prefix_bytes(int B) { return ((size_t)B * 8 + 8 + 15) / 16 * 16; }
 
 size_t workspace_for(const DeviceView &dv, int B, int G, int Nq, int D) {
-  const int t = few_rows(G, Nq) ? tile_rows(G, Nq) : kChunkRows;
-  return prefix_bytes(B) + (size_t)run_count(dv, G, Nq) * 2 * t * (D + 4) * sizeof(float);
+  const int tiles = row_tiles(G, Nq, D);
+  const int rows = tiles ? 8 * tiles : kChunkRows;
+  return prefix_bytes(B) + (size_t)run_count(dv, tiles, D) * 2 * rows * (D + 4) * sizeof(float);
 }
 
 template <int D, int kNT>
@@ -370,18 +381,29 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
   p.Nq = Nq;
   p.causal = causal != 0;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.tile_rows = tile_rows(p.G, Nq);
-  p.ctas = run_count(dv, p.G, Nq);
+  const int tiles = row_tiles(p.G, Nq, D);
+  p.tile_rows = 8 * tiles;
+  p.ctas = run_count(dv, tiles, D);
   p.err = dv.err_word;
   p.prefix = static_cast<long long *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + prefix_bytes(B));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (!few_rows(p.G, Nq))
-    e = D == 64 ? launch_chunk<64>(p, s) : launch_chunk<128>(p, s);
-  else if (p.tile_rows == 8)
-    e = D == 64 ? launch_decode<64, 1>(p, s) : launch_decode<128, 1>(p, s);
-  else
-    e = D == 64 ? launch_decode<64, 2>(p, s) : launch_decode<128, 2>(p, s);
+  if (D == 64) {
+    switch (tiles) {
+      case 0: e = launch_chunk<64>(p, s); break;
+      case 1: e = launch_decode<64, 1>(p, s); break;
+      case 2: e = launch_decode<64, 2>(p, s); break;
+      case 3: e = launch_decode<64, 3>(p, s); break;
+      default: e = launch_decode<64, 5>(p, s); break;
+    }
+  } else {
+    switch (tiles) {
+      case 0: e = launch_chunk<128>(p, s); break;
+      case 1: e = launch_decode<128, 1>(p, s); break;
+      case 2: e = launch_decode<128, 2>(p, s); break;
+      default: e = launch_decode<128, 3>(p, s); break;
+    }
+  }
   return e == cudaSuccess ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }

@@ -13,8 +13,8 @@
 //    device; each CTA finds its run by a scan over the sequences).  A run that
 //    starts or ends inside a segment leaves a partial result (running maximum,
 //    sum and unnormalised O in fp32) that a second kernel merges.
-//  - A warp takes 16 positions of each unit, one run of 16 D bytes of keys and
-//    one of values (a page is a multiple of 16 positions), copied by cp.async
+//  - A warp takes 16 positions of each unit, 16 D bytes of keys and as many of
+//    values (a page is a multiple of 16 positions), copied by cp.async
 //    into its own ring: no barrier but the warp's own.  Rows are stored with
 //    their 16-byte pieces exchanged so that the operand loads are free of bank
 //    conflicts.  The order of a dot product's terms is free, so a lane's 16
@@ -72,7 +72,7 @@ struct Kv8AttnParams {
   unsigned g_mul;   // floor(2^32 / G) + 1, or 0 for G = 1
   int causal;
   float scale_log2;  // scale * log2(e)
-  int tile_rows;     // (few rows) 8 or 16, at least Nq * G
+  int tile_rows;     // (few rows) a tile's rows, at least Nq * G
   int ctas;          // runs the work is cut into
   int *err;
   float *part;       // [ctas, 2, rows of a tile or unit, D + 4]
@@ -86,7 +86,9 @@ constexpr float kDecTau = 8.f;       // m is exceeded by at most 2^8
 constexpr float kDecLift = 7.f;      // P' is lifted by 2^7
 constexpr float kDecNone = -1e30f;   // references before any score
 
-// kNT tiles of eight query rows.
+// kNT tiles of eight query rows a warp: up to 40 rows at D = 64 and 24 at
+// D = 128, where the accumulators (kNT * D / 4 a thread) still fit the registers.
+// From three tiles on, the queries' operands come from shared memory.
 template <int D, int kNT>
 struct DecCfg {
   static constexpr int kRows = 8 * kNT;
@@ -96,9 +98,12 @@ struct DecCfg {
   static constexpr int kRowStride = 8 * kRunStride + 4;
   static constexpr int kStageBytes = 16 * D * 2;  // a warp's keys and values of a unit
   static constexpr int kRingBytes = kDecWarps * kStages * kStageBytes;
-  static constexpr int kMergeBytes = kDecWarps * kRows * (kRowStride + 4) * 4;
-  static constexpr int kSmem = kRingBytes + kMergeBytes;
-  static constexpr int kCtasPerSm = kNT == 1 ? 3 : 2;
+  // the warps' parts of one tile of eight rows, and their statistics
+  static constexpr int kMergeBytes = kDecWarps * 8 * (kRowStride + 4) * 4;
+  static constexpr bool kQShared = kNT > 2;
+  static constexpr int kQBytes = kQShared ? kRows * (D * 2 + 4) : 0;  // operands, factors
+  static constexpr int kSmem = kRingBytes + kMergeBytes + kQBytes;
+  static constexpr int kCtasPerSm = D == 64 ? (kNT <= 1 ? 4 : kNT <= 3 ? 3 : 2) : (kNT == 1 ? 3 : 2);
 };
 
 // A sequence as the kernels use it.
@@ -341,7 +346,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   const Kv8Geom &g = p.g;
   const int segs = g.Hkv;  // segments of a sequence
   float *merge_o = reinterpret_cast<float *>(smem + C::kRingBytes);
-  float *merge_s = merge_o + kDecWarps * C::kRows * C::kRowStride;  // m, M, l of each warp's rows
+  float *merge_s = merge_o + kDecWarps * 8 * C::kRowStride;  // m, M, l of each warp's rows
+  uint4 *q_ops = reinterpret_cast<uint4 *>(smem + C::kRingBytes + C::kMergeBytes);
+  float *q_fac = reinterpret_cast<float *>(q_ops + kNT * (kSteps / 2) * 32);  // of each row
 
   grid_wait();
   grid_launch_dependents();  // (after the wait: the merge reads the lengths before its own)
@@ -395,12 +402,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   auto issue = [&](int stage, int id) -> int {
     if (!kv8_page_ok(g, id)) {
       if (id != -2 && lane == 0) atomicCAS(p.err, 0, kDevErrIndex);
-      cp_async_commit();
       return -1;
     }
-    const int h = prod.seg;
     const int t = prod.unit * kDecUnit + warp * 16;
-    const int eoff = id * g.Hkv + h;  // (the host bounds num_pages * Hkv)
+    const int eoff = id * g.Hkv + prod.seg;  // (the host bounds num_pages * Hkv)
     const long long off = (long long)eoff * (g.page * D) + (t & (g.page - 1)) * D;
     const uint8_t *ks = p.k + off + lane * 16, *vs = p.v + off + lane * 16;
     const uint32_t dk = ring + stage * C::kStageBytes;
@@ -411,7 +416,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       cp_async16(d, ks + i * 512);
       cp_async16(d + 16 * D, vs + i * 512);
     }
-    cp_async_commit();
     return eoff;
   };
 
@@ -421,14 +425,13 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   int next_id = fetch_page();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
+    eo[s] = -1;
     if (s < nsteps) {
       eo[s] = issue(s, next_id);
       dec_advance(p, prod, segs);
       next_id = s + 1 < nsteps ? fetch_page() : -2;
-    } else {
-      cp_async_commit();
-      eo[s] = -1;
     }
+    cp_async_commit();
   }
   int eo_now = eo[0];
   int ke_now = eo_now >= 0 ? p.ke[eo_now] : 0, ve_now = eo_now >= 0 ? p.ve[eo_now] : 0;
@@ -443,14 +446,16 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     bool bad = false;
     const int rows = seq_rows(p, b, &bad);
     const int r_end = rows * p.G;
+    const int vis_min = rows > 0 ? row_sees(p, 0, len, rows) : len;  // the first query's
     // Queries as the 8-wide operand: this lane holds parts of rows 8 t + q8,
     // and the statistics of rows 8 t + 2 c4 and 8 t + 2 c4 + 1.
-    int vis[kNT][2];
-    float f[kNT][2];
-    uint32_t qf[kNT][kSteps][2];
-    int vis_min = len;
+    float f[C::kQShared ? 1 : kNT][2] = {};
+    uint32_t qf[C::kQShared ? 1 : kNT][kSteps][2];
+    if constexpr (C::kQShared) __syncthreads();  // the last segment's are read
 #pragma unroll
-    for (int t = 0; t < kNT; ++t) {
+    for (int t0 = 0; t0 < kNT; t0 += C::kQShared ? kDecWarps : 1) {
+      const int t = C::kQShared ? t0 + warp : t0;  // (shared: a warp a tile)
+      if (C::kQShared && t >= kNT) break;
       const int r = 8 * t + q8;
       const bool on = r < r_end;
       const int i = row_query(p, r);
@@ -472,20 +477,34 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       ea = min(ea, 126);
       const float sc = exp2i(-ea);
       const float fr = p.scale_log2 * exp2i(ea);
+      if constexpr (C::kQShared) {
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) {
-        qf[t][ks][0] = bf16x2_to_f16x2_scaled(w[ks].x, sc);
-        qf[t][ks][1] = bf16x2_to_f16x2_scaled(w[ks].y, sc);
-      }
+        for (int ks = 0; ks < kSteps; ks += 2)
+          q_ops[(t * (kSteps / 2) + ks / 2) * 32 + lane] =
+              make_uint4(bf16x2_to_f16x2_scaled(w[ks].x, sc), bf16x2_to_f16x2_scaled(w[ks].y, sc),
+                         bf16x2_to_f16x2_scaled(w[ks + 1].x, sc),
+                         bf16x2_to_f16x2_scaled(w[ks + 1].y, sc));
+        if (c4 == 0) q_fac[r] = fr;
+      } else {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int rx = 8 * t + 2 * c4 + x;
-        vis[t][x] = rx < r_end ? row_sees(p, row_query(p, rx), len, rows) : 0;
-        vis_min = min(vis_min, rx < r_end ? vis[t][x] : len);
-        f[t][x] = __shfl_sync(0xffffffffu, fr, (2 * c4 + x) * 4);
+        for (int ks = 0; ks < kSteps; ++ks) {
+          qf[t][ks][0] = bf16x2_to_f16x2_scaled(w[ks].x, sc);
+          qf[t][ks][1] = bf16x2_to_f16x2_scaled(w[ks].y, sc);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) f[t][x] = __shfl_sync(0xffffffffu, fr, (2 * c4 + x) * 4);
       }
     }
-    vis_min = __reduce_min_sync(0xffffffffu, vis_min);
+    if constexpr (C::kQShared) __syncthreads();
+    // factor of a row of this lane's, and the positions it sees
+    auto factor = [&](int t, int x) -> float {
+      if constexpr (C::kQShared) return q_fac[8 * t + 2 * c4 + x];
+      return f[C::kQShared ? 0 : t][x];
+    };
+    auto sees = [&](int t, int x) -> int {
+      const int r = 8 * t + 2 * c4 + x;
+      return r < r_end ? row_sees(p, row_query(p, r), len, rows) : 0;
+    };
 
     float o[kNT][kSteps][4];
     float m[kNT][2], mo[kNT][2], l[kNT][2];
@@ -501,7 +520,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     for (int n = 0; n < n_here; ++n, ++step) {
       // issue the step kStages - 1 ahead, then wait for this one's copies
       const bool none = eo_now < 0;
-      const int ke = ke_now, ve = ve_now;
+      const float fk = exp2i(max(ke_now, -126)), ev = (float)ve_now;
       eo_now = eo[1];
       int eo_new = -1;
       const int ahead = stage == 0 ? kStages - 1 : stage - 1;
@@ -509,9 +528,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
         eo_new = issue(ahead, next_id);
         dec_advance(p, prod, segs);
         next_id = step + kStages < nsteps ? fetch_page() : -2;
-      } else {
-        cp_async_commit();
       }
+      cp_async_commit();
 #pragma unroll
       for (int i = 0; i + 1 < kStages - 1; ++i) eo[i] = eo[i + 1];
       eo[kStages - 2] = eo_new;
@@ -523,8 +541,6 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       stage = stage == kStages - 1 ? 0 : stage + 1;
       const int t0 = (cons.unit + n) * kDecUnit + warp * 16;
       if (none) continue;  // no positions of this warp (warp-uniform)
-      const float fk = exp2i(max(ke, -126));
-      const float ev = (float)ve;
 
       // S^T = K Q^T: 16 positions x 8 rows a tile; s[t][0, 1]: position q8,
       // rows 2 c4 and 2 c4 + 1; s[t][2, 3]: position q8 + 8
@@ -542,39 +558,46 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
           e4m3x4_to_f16x2x2(x0[i], a0, a2);
           e4m3x4_to_f16x2x2(x1[i], a1, a3);
 #pragma unroll
-          for (int t = 0; t < kNT; ++t)
-            mma_f16(s[t], a0, a1, a2, a3, qf[t][4 * j + i][0], qf[t][4 * j + i][1]);
+          for (int t = 0; t < kNT; ++t) {
+            if constexpr (C::kQShared) {
+              const uint2 qv = reinterpret_cast<const uint2 *>(
+                  q_ops + (t * (kSteps / 2) + 2 * j + i / 2) * 32 + lane)[i & 1];
+              mma_f16(s[t], a0, a1, a2, a3, qv.x, qv.y);
+            } else {
+              mma_f16(s[t], a0, a1, a2, a3, qf[t][4 * j + i][0], qf[t][4 * j + i][1]);
+            }
+          }
         }
       }
       const bool edge = t0 + 16 > vis_min;
-      // z = s - m (log2 units), and how far m + ve lies above M: while no
-      // score passes m by more than 2^tau and no m + ve passes M, the
-      // references stay and nothing has to be reduced across the warp.
-      float z[kNT][4], over[kNT][2];
+      // z = s - m (log2 units); while no score passes m by more than 2^tau and
+      // no m + ve passes M, the references stay and nothing has to be reduced
+      // across the warp.
+      float z[kNT][4];
       float top = -1.f;
 #pragma unroll
       for (int t = 0; t < kNT; ++t)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float fx = f[t][x] * fk;
+          const float fx = factor(t, x) * fk;
           z[t][x] = fmaf(s[t][x], fx, -m[t][x]);
           z[t][2 + x] = fmaf(s[t][2 + x], fx, -m[t][x]);
           if (edge) {
-            if (t0 + q8 >= vis[t][x]) z[t][x] = -INFINITY;
-            if (t0 + q8 + 8 >= vis[t][x]) z[t][2 + x] = -INFINITY;
+            const int see = sees(t, x);
+            if (t0 + q8 >= see) z[t][x] = -INFINITY;
+            if (t0 + q8 + 8 >= see) z[t][2 + x] = -INFINITY;
           }
-          over[t][x] = m[t][x] + ev - mo[t][x];
-          top = fmaxf(top, max3(z[t][x] - kDecTau, z[t][2 + x] - kDecTau, over[t][x]));
+          top = fmaxf(top, max3(z[t][x] - kDecTau, z[t][2 + x] - kDecTau,
+                                m[t][x] + ev - mo[t][x]));
         }
       if (__any_sync(0xffffffffu, top > 0.f)) {
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float fx = f[t][x] * fk;
+            const float fx = factor(t, x) * fk;
             const bool see0 = z[t][x] != -INFINITY, see1 = z[t][2 + x] != -INFINITY;
-            const float y0 = s[t][x] * fx, y1 = s[t][2 + x] * fx;
-            float mx = fmaxf(see0 ? y0 : -INFINITY, see1 ? y1 : -INFINITY);
+            float mx = fmaxf(see0 ? s[t][x] * fx : -INFINITY, see1 ? s[t][2 + x] * fx : -INFINITY);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -583,10 +606,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
             m[t][x] = m_new;
             if (see0) z[t][x] = fmaf(s[t][x], fx, -m_new);
             if (see1) z[t][2 + x] = fmaf(s[t][2 + x], fx, -m_new);
-            const float mo_new = fmaxf(mo[t][x], m[t][x] + ev);
+            const float mo_new = fmaxf(mo[t][x], m_new + ev);
             const float up = ex2_approx(mo[t][x] - mo_new);
             mo[t][x] = mo_new;
-            over[t][x] = m[t][x] + ev - mo_new;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
               o[t][j][x] *= up;
@@ -601,7 +623,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           // P = 2^(s - m), P' = P 2^(m + ve - M + lift)
-          const float lift = ex2_approx(over[t][x] + kDecLift);
+          const float lift = ex2_approx(m[t][x] + ev - mo[t][x] + kDecLift);
           const float e0 = ex2_approx(z[t][x]), e1 = ex2_approx(z[t][2 + x]);
           l[t][x] += e0 + e1;
           pr[x] = e0 * lift;
@@ -629,6 +651,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
         }
       }
       __syncwarp();  // this step's slot is read: the next copies may take it
+      bool by_query = false;
       if (edge) {
         bool odd = false;
 #pragma unroll
@@ -640,86 +663,89 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
             odd |= tok >= vis_min && has_nan4(w[i][y]);
           }
         }
-        if (__any_sync(0xffffffffu, odd)) {
-          // query by query, without the positions that one does not see
+        by_query = __any_sync(0xffffffffu, odd);
+      }
+      if (!by_query) {
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2x2(__byte_perm(w[0][j >> 1], w[1][j >> 1], sel), a0, a1);
+          e4m3x4_to_f16x2x2(__byte_perm(w[2][j >> 1], w[3][j >> 1], sel), a2, a3);
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) mma_f16(o[t][j], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+        }
+      } else {
+        // a NaN that some rows see and others do not: query by query, without
+        // the positions that one does not see
 #pragma unroll 1
-          for (int i = 0; i < rows; ++i) {
-            const int see = row_sees(p, i, len, rows);
-            uint32_t z[4][kVw];
+        for (int i = 0; i < rows; ++i) {
+          const int see = row_sees(p, i, len, rows);
+          uint32_t v[4][kVw];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int y = 0; y < kVw; ++y)
-                z[k][y] = t0 + 2 * c4 + (k & 1) + (k >> 1) * 8 < see ? w[k][y] : 0u;
+            for (int y = 0; y < kVw; ++y)
+              v[k][y] = t0 + 2 * c4 + (k & 1) + (k >> 1) * 8 < see ? w[k][y] : 0u;
 #pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-              const int ra = 8 * t + 2 * c4;
-              const bool on0 = row_query(p, ra) == i, on1 = row_query(p, ra + 1) == i;
+          for (int t = 0; t < kNT; ++t) {
+            const int ra = 8 * t + 2 * c4;
+            const bool on0 = row_query(p, ra) == i, on1 = row_query(p, ra + 1) == i;
 #pragma unroll
-              for (int j = 0; j < kSteps; ++j) {
-                const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_to_f16x2x2(__byte_perm(z[0][j >> 1], z[1][j >> 1], sel), a0, a1);
-                e4m3x4_to_f16x2x2(__byte_perm(z[2][j >> 1], z[3][j >> 1], sel), a2, a3);
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(d, a0, a1, a2, a3, pb[t][0], pb[t][1]);
-                if (on0) {
-                  o[t][j][0] += d[0];
-                  o[t][j][2] += d[2];
-                }
-                if (on1) {
-                  o[t][j][1] += d[1];
-                  o[t][j][3] += d[3];
-                }
+            for (int j = 0; j < kSteps; ++j) {
+              const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x2x2(__byte_perm(v[0][j >> 1], v[1][j >> 1], sel), a0, a1);
+              e4m3x4_to_f16x2x2(__byte_perm(v[2][j >> 1], v[3][j >> 1], sel), a2, a3);
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(d, a0, a1, a2, a3, pb[t][0], pb[t][1]);
+              if (on0) {
+                o[t][j][0] += d[0];
+                o[t][j][2] += d[2];
+              }
+              if (on1) {
+                o[t][j][1] += d[1];
+                o[t][j][3] += d[3];
               }
             }
           }
-          continue;
         }
-      }
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
-        uint32_t a0, a1, a2, a3;
-        e4m3x4_to_f16x2x2(__byte_perm(w[0][j >> 1], w[1][j >> 1], sel), a0, a1);
-        e4m3x4_to_f16x2x2(__byte_perm(w[2][j >> 1], w[3][j >> 1], sel), a2, a3);
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) mma_f16(o[t][j], a0, a1, a2, a3, pb[t][0], pb[t][1]);
       }
     }
 
     // ---------------------------------------------------------- join the warps
-    __syncthreads();  // the merge buffer is free
+    // a tile of eight rows at a time
 #pragma unroll
-    for (int t = 0; t < kNT; ++t)
+    for (int t = 0; t < kNT; ++t) {
+      if (8 * t >= r_end) break;
+      __syncthreads();  // the merge buffer is free
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float ls = l[t][x];
         ls += __shfl_xor_sync(0xffffffffu, ls, 4);
         ls += __shfl_xor_sync(0xffffffffu, ls, 8);
         ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-        const int row = 8 * t + 2 * c4 + x;
+        const int row = 2 * c4 + x;
         if (q8 == 0)
-          *reinterpret_cast<float4 *>(merge_s + (warp * C::kRows + row) * 4) =
+          *reinterpret_cast<float4 *>(merge_s + (warp * 8 + row) * 4) =
               make_float4(m[t][x], mo[t][x], ls, 0.f);
-        float *d = merge_o + (warp * C::kRows + row) * C::kRowStride + q8 * C::kRunStride;
+        float *d = merge_o + (warp * 8 + row) * C::kRowStride + q8 * C::kRunStride;
 #pragma unroll
         for (int j = 0; j < kSteps; j += 2)
           *reinterpret_cast<float4 *>(d + 2 * j) = make_float4(
               o[t][j][x], o[t][j][2 + x], o[t][j + 1][x], o[t][j + 1][2 + x]);
       }
-    __syncthreads();
-    {
-      constexpr int kPer = kDecThreads / C::kRows;  // threads of a row
-      constexpr int kCols = D / kPer;               // columns of a thread
+      __syncthreads();
+      constexpr int kPer = kDecThreads / 8;  // threads of a row
+      constexpr int kCols = D / kPer;        // columns of a thread
       const int row = threadIdx.x / kPer, col = (threadIdx.x % kPer) * kCols;
-      const int r = row;
+      const int r = 8 * t + row;
       if (r < r_end) {
         float mm = kDecNone, mmo = kDecNone, ll = 0.f;
         float4 st[kDecWarps];
 #pragma unroll
         for (int w2 = 0; w2 < kDecWarps; ++w2) {
-          st[w2] = *reinterpret_cast<const float4 *>(merge_s + (w2 * C::kRows + row) * 4);
+          st[w2] = *reinterpret_cast<const float4 *>(merge_s + (w2 * 8 + row) * 4);
           mm = fmaxf(mm, st[w2].x);
           mmo = fmaxf(mmo, st[w2].y);
         }
@@ -734,7 +760,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
           const bool none = st[w2].z == 0.f;
           ll += none ? 0.f : st[w2].z * ex2_approx(st[w2].x - mm);
           const float wt = none ? 0.f : ex2_approx(st[w2].y - mmo);
-          const float *d = d0 + w2 * C::kRows * C::kRowStride;
+          const float *d = d0 + w2 * 8 * C::kRowStride;
 #pragma unroll
           for (int j = 0; j < kCols; j += 4) {
             const float4 y = *reinterpret_cast<const float4 *>(d + j);
@@ -759,7 +785,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
             p.lse[orow] =
                 ll == 0.f ? -INFINITY : (mm + lg2_approx(ll)) * 0.69314718055994531f;
         } else {
-          float *d = p.part + (((size_t)blockIdx.x * 2 + (seg_index > 0)) * C::kRows + row) *
+          float *d = p.part + (((size_t)blockIdx.x * 2 + (seg_index > 0)) * C::kRows + r) *
                                   (D + 4);
 #pragma unroll
           for (int j = 0; j < kCols; j += 4)

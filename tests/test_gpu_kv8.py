@@ -216,6 +216,13 @@ CASES = [
     ([33] * 300, 1, 2, 1, None, 16, 64, True),      # more sequences than a scan's width
     ([700] * 3, 2, 7, 40, None, 64, 128, True),
     ([700] * 2, 1, 96, 3, None, 64, 64, True),
+    # between one tile of rows and the tensor core's: three to eight tiles of eight
+    ([600, 77, 0], 2, 8, 3, None, 16, 64, True),
+    ([600, 77, 1], 2, 6, 4, [4, 0, 1], 32, 128, True),
+    ([2000, 300], 2, 8, 5, None, 32, 64, True),
+    ([2000, 300], 1, 4, 8, [8, 5], 64, 128, False),
+    ([900, 130], 2, 7, 9, None, 16, 64, True),
+    ([900, 130], 1, 10, 5, None, 128, 128, True),
 ]
 
 
@@ -255,7 +262,7 @@ def test_pages_of_very_different_magnitude(tk_lib, Nq, G):
     check(q, cache, table, [n], None, True, D ** -0.5, o, lse)
 
 
-@pytest.mark.parametrize("Nq,G", [(1, 2), (4, 3), (60, 4), (300, 1)])
+@pytest.mark.parametrize("Nq,G", [(1, 2), (4, 3), (5, 5), (60, 4), (300, 1)])
 @pytest.mark.parametrize("which", ["k", "v"])
 def test_nan_in_masked_positions_has_no_effect(tk_lib, Nq, G, which):
     """Rows behind the length, and later positions of the same call, may hold
