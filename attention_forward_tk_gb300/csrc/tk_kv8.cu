@@ -294,6 +294,12 @@ cudaError_t launch_chunk(const Kv8AttnParams &p, cudaStream_t s) {
   const cudaError_t e = launch_overlapped(tk_kv8_chunk_kernel<D>, p.ctas, kChunkThreads,
                                           ChunkCfg<D>::kSmemAlloc, s, tk, tv, p);
   if (e != cudaSuccess) return e;
+  // Four runs a unit or more on average: the partials of a row are the parallel
+  // work; else the rows are.
+  const long long units = (long long)p.B * p.g.Hkv * (((long long)p.Nq * p.G + 255) / 256);
+  if (4 * units <= p.ctas)
+    return launch_overlapped(tk_kv8_chunk_merge_deep_kernel<D>,
+                             dim3((unsigned)(p.Nq * p.G), p.g.Hkv, p.B), kMergeWarps * 32, 0, s, p);
   return launch_overlapped(tk_kv8_chunk_merge_kernel<D>,
                            dim3((unsigned)(((long long)p.Nq * p.G + 31) / 32), p.g.Hkv, p.B), 256, 0,
                            s, p);

@@ -746,10 +746,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               }
             }
             if (ok) {
-              if (pwhole)
+              if (pwhole) {
                 p.lse[orow] = lse;
-              else
-                part_row[D] = lse;
+              } else {  // as merge_row takes it: O is normalised, so l is 1 or nothing
+                const float m2 = l == 0.f ? -INFINITY : m + lg2_approx(l);
+                *reinterpret_cast<float4 *>(part_row + D) =
+                    make_float4(m2, m2 + kDecLift, l == 0.f ? 0.f : m2 == m2 ? 1.f : m2, 0.f);
+              }
               if (nan) {  // columns in which this row sees a NaN
 #pragma unroll 1
                 for (int k = 0; k < D; ++k)
@@ -1074,21 +1077,36 @@ done:
   }
 }
 
-// Merge of the runs' partial results (O / l and LSE of a run): a warp takes four
-// rows of one tile, all their partials of a run in flight together.
-// grid: (ceil(Nq * G / 32), Hkv, B)
-constexpr int kChunkMergeRows = 4;
-template <int D>
-__global__ void __launch_bounds__(256)
-    tk_kv8_chunk_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
-  constexpr int kPer = D / 32;
-  const int b = blockIdx.z, h = blockIdx.y;
-  const int lane = threadIdx.x & 31;
-  const int r0 = blockIdx.x * (8 * kChunkMergeRows) + (threadIdx.x >> 5) * kChunkMergeRows;
-  const ChunkSeq s = chunk_seq(p, b);
-  const int mb = r0 / kChunkRows, r_end = s.rows * p.G;
-  // steps of the head's units before these rows', and of all of them
-  long long before = 0, all = 0;
+// Where a unit's partials lie: runs [c0, c1], of which c0's is its slot `first`;
+// c0 == c1: one run held the unit whole.  `before` and `all`: steps of the
+// head's units before unit mb, and of all of them (after grid_wait).
+struct ChunkParts {
+  int c0, c1, first;
+};
+__device__ __forceinline__ ChunkParts chunk_parts(const Kv8AttnParams &p, const ChunkSeq &s, int b,
+                                                  int h, int mb, int tile_first, long long before,
+                                                  long long all) {
+  const long long share = p.prefix[p.B];
+  const long long s0 = p.prefix[b] + h * all + before;
+  ChunkParts r;
+  r.c0 = (int)(s0 / share);
+  r.c1 = (int)((s0 + chunk_cost(p, s, mb) - 1) / share);
+  r.first = r.c0 * share == s0 ? 0 : 1;
+  // runs that hold no key tile of the row's tile wrote nothing for it
+  if (r.c0 != r.c1) {
+    const int tiles = chunk_tiles(p, tile_first, s.len, s.rows);
+    const int end = (int)((s0 + tiles - 1) / share);
+    // (all in the first run: still a partial, joined alone)
+    r.c1 = end < r.c1 ? end : r.c1;
+    if (r.c1 == r.c0) r.c1 = -1 - r.c0;
+  }
+  return r;
+}
+
+// Steps of a head's units before unit mb, and of all: a warp.
+__device__ __forceinline__ void chunk_before(const Kv8AttnParams &p, const ChunkSeq &s, int mb,
+                                             int lane, long long &before, long long &all) {
+  before = all = 0;
 #pragma unroll 1
   for (int x = lane; x < s.units; x += 32) {
     const int c = chunk_cost(p, s, x);
@@ -1100,19 +1118,48 @@ __global__ void __launch_bounds__(256)
     before += __shfl_xor_sync(0xffffffffu, before, d);
     all += __shfl_xor_sync(0xffffffffu, all, d);
   }
+}
+
+// Merge where units lie in many runs: a block a row.  grid: (Nq * G, Hkv, B)
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    tk_kv8_chunk_merge_deep_kernel(const __grid_constant__ Kv8AttnParams p) {
+  const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const ChunkSeq s = chunk_seq(p, b);
+  const int mb = r / kChunkRows;
+  long long before, all;
+  chunk_before(p, s, mb, threadIdx.x & 31, before, all);
+  grid_wait();  // (above: only what the launch before leaves alone)
+  if (r >= s.rows * p.G) return;
+  const ChunkParts c = chunk_parts(p, s, b, h, mb, r / 128 * 128, before, all);
+  if (c.c0 == c.c1) return;
+  const int i = row_query(p, r);
+  const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
+  merge_row<D>(p.part + (size_t)(r % kChunkRows) * (D + 4), (size_t)kChunkRows * (D + 4), c.c0,
+               c.c1 < 0 ? c.c0 : c.c1, c.first, p.o + orow * D, p.lse + orow);
+}
+
+// Merge where units lie in few runs: a warp takes four rows of one tile, all
+// their partials of a run in flight together.  grid: (ceil(Nq * G / 32), Hkv, B)
+constexpr int kChunkMergeRows = 4;
+template <int D>
+__global__ void __launch_bounds__(256)
+    tk_kv8_chunk_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
+  constexpr int kPer = D / 32;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  const int r0 = blockIdx.x * (8 * kChunkMergeRows) + (threadIdx.x >> 5) * kChunkMergeRows;
+  const ChunkSeq s = chunk_seq(p, b);
+  const int mb = r0 / kChunkRows, r_end = s.rows * p.G;
+  long long before, all;
+  chunk_before(p, s, mb, lane, before, all);
   grid_wait();  // (above: only what the launch before leaves alone)
   if (r0 >= r_end) return;
-  const long long share = p.prefix[p.B];
-  const long long s0 = p.prefix[b] + h * all + before;
-  const int cost = chunk_cost(p, s, mb);
-  const int c0 = (int)(s0 / share), c1 = (int)((s0 + cost - 1) / share);
-  if (c0 == c1) return;
-  // runs that hold no key tile of these rows' tile wrote nothing for them
-  const int tiles = chunk_tiles(p, r0 / 128 * 128, s.len, s.rows);
-  const int c_end = min(c1, (int)((s0 + tiles - 1) / share));
+  const ChunkParts at = chunk_parts(p, s, b, h, mb, r0 / 128 * 128, before, all);
+  if (at.c0 == at.c1) return;
+  const int c_end = at.c1 < 0 ? at.c0 : at.c1;
   const size_t slot = (size_t)kChunkRows * (D + 4);
   const float *base = p.part + (size_t)(r0 % kChunkRows) * (D + 4);
-  const int first0 = c0 * share == s0 ? 0 : 1;
   float mx[kChunkMergeRows], z[kChunkMergeRows], acc[kChunkMergeRows][kPer];
 #pragma unroll
   for (int i = 0; i < kChunkMergeRows; ++i) {
@@ -1122,8 +1169,8 @@ __global__ void __launch_bounds__(256)
     for (int k = 0; k < kPer; ++k) acc[i][k] = 0.f;
   }
 #pragma unroll 2
-  for (int c = c0; c <= c_end; ++c) {
-    const float *d = base + ((size_t)c * 2 + (c == c0 ? first0 : 0)) * slot;
+  for (int c = at.c0; c <= c_end; ++c) {
+    const float *d = base + ((size_t)c * 2 + (c == at.c0 ? at.first : 0)) * slot;
     float l[kChunkMergeRows], x[kChunkMergeRows][kPer];
 #pragma unroll
     for (int i = 0; i < kChunkMergeRows; ++i) {
@@ -1131,7 +1178,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int k = 0; k < kPer; ++k) x[i][k] = 0.f;
       if (r0 + i < r_end) {
-        l[i] = d[i * (D + 4) + D];
+        l[i] = d[i * (D + 4) + D];  // log2 of the run's sum
 #pragma unroll
         for (int k = 0; k < kPer; ++k) x[i][k] = d[i * (D + 4) + lane * kPer + k];
       }
@@ -1139,7 +1186,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 0; i < kChunkMergeRows; ++i) {
       const float m = fmaxf(mx[i], l[i]);
-      const float up = expf(mx[i] - m), w = expf(l[i] - m);  // (l -inf: 0; NaN stays)
+      const float up = exp2f(mx[i] - m), w = exp2f(l[i] - m);  // (l none: 0; NaN stays)
       mx[i] = m;
       z[i] = fmaf(z[i], up, w);
 #pragma unroll
@@ -1157,7 +1204,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int k = 0; k < kPer / 2; ++k)
       dst[k] = pack_bf16x2(acc[i][2 * k] * inv, acc[i][2 * k + 1] * inv);
-    if (lane == 0) p.lse[orow] = z[i] == 0.f ? -INFINITY : mx[i] + logf(z[i]);
+    if (lane == 0) p.lse[orow] =
+          z[i] == 0.f ? -INFINITY : (mx[i] + log2f(z[i])) * 0.69314718055994531f;
   }
 }
 

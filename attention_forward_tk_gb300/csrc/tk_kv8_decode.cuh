@@ -802,56 +802,17 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   }
 }
 
-// Merge of the runs' partial results: a block for each (head, sequence, row).
-// A warp takes every eighth partial, its lanes D/32 columns each; then the warps
-// are joined.  Segments that one run held whole are already written.
+// One row's partials [c0, c1] joined by a block: a warp takes every eighth, its
+// lanes D/32 columns each; then the warps.  A partial is O relative to 2^M, with
+// m, M and l behind it (all relative to the same row's); c0's is at `first`.
 constexpr int kMergeWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
-    tk_kv8_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
+__device__ __forceinline__ void merge_row(const float *base, size_t slot, int c0, int c1,
+                                          int first, __nv_bfloat16 *o, float *lse) {
   constexpr int kPer = D / 32;
-  __shared__ int red[2][kMergeWarps];
   __shared__ float stat[kMergeWarps][3];
   __shared__ float cols[kMergeWarps][D];
-  // (It does not let its dependents begin: the next call's runs, resident early,
-  // would take the registers that these blocks need; 161 -> 228 us at 8 x 16384.)
-  const int h = blockIdx.x, b = blockIdx.y, r = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  bool bad = false;
-  const int rows = seq_rows(p, b, &bad);
-  // the units before this sequence, and all of them
-  int before = 0, total = 0;
-#pragma unroll 1
-  for (int x = threadIdx.x; x < p.B; x += kMergeWarps * 32) {
-    const int v = seq_units(p, x, kDecUnit) * p.g.Hkv;
-    total += v;
-    if (x < b) before += v;
-  }
-  before = __reduce_add_sync(0xffffffffu, before);
-  total = __reduce_add_sync(0xffffffffu, total);
-  if (lane == 0) {
-    red[0][warp] = before;
-    red[1][warp] = total;
-  }
-  __syncthreads();
-  before = total = 0;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    before += red[0][w];
-    total += red[1][w];
-  }
-  const int units = seq_units(p, b, kDecUnit);
-  const int share = max(1, (int)(((unsigned)total + p.ctas - 1) / (unsigned)p.ctas));
-  const int s0 = before + h * units;
-  const int c0 = s0 / share, c1 = (s0 + max(units, 1) - 1) / share;
-  // run c0's partial is its first segment's only if it starts where the segment does
-  const int first0 = c0 * share == s0 ? 0 : 1;
-  const float *base = p.part + (size_t)r * (D + 4);
-  const size_t slot = (size_t)p.tile_rows * (D + 4);
-  // All above reads only what the launch before leaves alone, and what came
-  // before that one has ended (it starts this one after its own wait).
-  grid_wait();
-  if (r >= rows * p.G || c0 == c1) return;
   float mm = kDecNone, mmo = kDecNone, ll = 0.f, acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
@@ -865,7 +826,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       const int ci = c + i * kMergeWarps;
       st[i] = make_float4(kDecNone, kDecNone, 0.f, 0.f);
       if (ci <= c1) {
-        const float *d = base + ((size_t)ci * 2 + (ci == c0 ? first0 : 0)) * slot;
+        const float *d = base + ((size_t)ci * 2 + (ci == c0 ? first : 0)) * slot;
         st[i] = *reinterpret_cast<const float4 *>(d + D);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) x[i][k] = d[lane * kPer + k];
@@ -916,13 +877,61 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     ll += stat[w][2] * ex2_approx(stat[w][0] - mm);
     out = fmaf(ex2_approx(stat[w][1] - mmo), cols[w][threadIdx.x], out);
   }
-  const int i = row_query(p, r);
-  const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
   const float half = ll == 0.f ? 0.f : ex2_approx(0.5f * (mmo - kDecLift - mm));
   const float inv = ll == 0.f ? 0.f : half / ll;
-  p.o[orow * D + threadIdx.x] = __float2bfloat16(out * inv * half);
+  o[threadIdx.x] = __float2bfloat16(out * inv * half);
   if (threadIdx.x == 0)
-    p.lse[orow] = ll == 0.f ? -INFINITY : (mm + lg2_approx(ll)) * 0.69314718055994531f;
+    *lse = ll == 0.f ? -INFINITY : (mm + lg2_approx(ll)) * 0.69314718055994531f;
+}
+
+// Merge of the runs' partial results: a block for each (head, sequence, row).
+// Segments that one run held whole are already written.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    tk_kv8_merge_kernel(const __grid_constant__ Kv8AttnParams p) {
+  __shared__ int red[2][kMergeWarps];
+  // (It does not let its dependents begin: the next call's runs, resident early,
+  // would take the registers that these blocks need; 161 -> 228 us at 8 x 16384.)
+  const int h = blockIdx.x, b = blockIdx.y, r = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool bad = false;
+  const int rows = seq_rows(p, b, &bad);
+  // the units before this sequence, and all of them
+  int before = 0, total = 0;
+#pragma unroll 1
+  for (int x = threadIdx.x; x < p.B; x += kMergeWarps * 32) {
+    const int v = seq_units(p, x, kDecUnit) * p.g.Hkv;
+    total += v;
+    if (x < b) before += v;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) {
+    red[0][warp] = before;
+    red[1][warp] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    before += red[0][w];
+    total += red[1][w];
+  }
+  const int units = seq_units(p, b, kDecUnit);
+  const int share = max(1, (int)(((unsigned)total + p.ctas - 1) / (unsigned)p.ctas));
+  const int s0 = before + h * units;
+  const int c0 = s0 / share, c1 = (s0 + max(units, 1) - 1) / share;
+  // run c0's partial is its first segment's only if it starts where the segment does
+  const int first0 = c0 * share == s0 ? 0 : 1;
+  const float *base = p.part + (size_t)r * (D + 4);
+  const size_t slot = (size_t)p.tile_rows * (D + 4);
+  // All above reads only what the launch before leaves alone, and what came
+  // before that one has ended (it starts this one after its own wait).
+  grid_wait();
+  if (r >= rows * p.G || c0 == c1) return;
+  const int i = row_query(p, r);
+  const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
+  merge_row<D>(base, slot, c0, c1, first0, p.o + orow * D, p.lse + orow);
 }
 
 }  // namespace tkattn
