@@ -32,14 +32,14 @@ bool configure_decode() {
                               DecCfg<D, kNT>::kSmem) == cudaSuccess;
 }
 
-template <int D>
+template <int D, bool kPair>
 bool configure_chunk() {
-  if (cudaFuncSetAttribute(tk_kv8_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(tk_kv8_chunk_kernel<D, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            ChunkCfg<D>::kSmemAlloc) != cudaSuccess)
     return false;
   // the register split between warpgroups assumes exactly 128 a thread at launch
   cudaFuncAttributes fa;
-  return cudaFuncGetAttributes(&fa, tk_kv8_chunk_kernel<D>) == cudaSuccess && fa.numRegs == 128;
+  return cudaFuncGetAttributes(&fa, tk_kv8_chunk_kernel<D, kPair>) == cudaSuccess && fa.numRegs == 128;
 }
 
 int kv8_device(DeviceView *dv) {
@@ -50,7 +50,8 @@ int kv8_device(DeviceView *dv) {
     d.ok = configure_decode<64, 1>() && configure_decode<64, 2>() && configure_decode<64, 3>() &&
            configure_decode<64, 5>() && configure_decode<128, 1>() && configure_decode<128, 2>() &&
            configure_decode<128, 3>() &&
-           configure_chunk<64>() && configure_chunk<128>();
+           configure_chunk<64, false>() && configure_chunk<128, false>() &&
+           configure_chunk<64, true>() && configure_chunk<128, true>();
   });
   return d.ok ? TK_ATTN_OK : TK_ATTN_ERR_LAUNCH;
 }
@@ -291,8 +292,9 @@ cudaError_t launch_chunk(const Kv8AttnParams &p, cudaStream_t s) {
   CUtensorMap tk, tv;
   if (!make_map_bytes(&tk, p.k, rows, D, p.g.page) || !make_map_bytes(&tv, p.v, rows, D, p.g.page))
     return cudaErrorInvalidValue;
-  const cudaError_t e = launch_overlapped(tk_kv8_chunk_kernel<D>, p.ctas, kChunkThreads,
-                                          ChunkCfg<D>::kSmemAlloc, s, tk, tv, p);
+  const cudaError_t e =
+      launch_overlapped(p.pair ? tk_kv8_chunk_kernel<D, true> : tk_kv8_chunk_kernel<D, false>,
+                        p.ctas, kChunkThreads, ChunkCfg<D>::kSmemAlloc, s, tk, tv, p);
   if (e != cudaSuccess) return e;
   // Four runs a unit or more on average: the partials of a row are the parallel
   // work; else the rows are.
@@ -389,6 +391,7 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   const int tiles = row_tiles(p.G, Nq, D);
   p.tile_rows = 8 * tiles;
+  p.pair = (long long)Nq * p.G <= 128;
   p.ctas = run_count(dv, tiles, D);
   p.err = dv.err_word;
   p.prefix = static_cast<long long *>(workspace);

@@ -26,6 +26,11 @@
 // the fp32 sum of the unrounded P, the rounding of each tile's largest P
 // carried into the divisor.
 //
+// With at most 128 rows a (sequence, head) (kPair) both tiles hold the same rows
+// and take every other key tile: a step is two key tiles, each tile of a run
+// leaves a partial result, and the softmax of one works beside the other's
+// products as it does with 256 rows.
+//
 // Roles (one CTA an SM, 512 threads):
 //   warps 0-3, 4-7  softmax of tile 0, 1; at a unit's start they convert their
 //                   tile's queries (their last scores being in hand, no product
@@ -78,8 +83,8 @@ struct ChunkCfg {
 // A segment: the part of one unit that lies in a CTA's run.
 struct ChunkSeg {
   int b, h, mb;     // mb < 0: the run is over
-  int j0, n;        // its key tiles
-  int n0, n1;       // how many of them each tile of queries visits
+  int j0, n;        // its steps
+  int n0, n1;       // how many of them each tile of queries takes part in
   int len, rows;    // of the sequence
   int whole;        // the unit lies in this run alone
 };
@@ -144,10 +149,11 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const Kv8AttnParams &p, int b) {
   s.units = (s.rows * p.G + kChunkRows - 1) / kChunkRows;
   return s;
 }
-// Key tiles of unit mb: those of its last row.
+// Steps of unit mb: the key tiles of its last row, or pairs of them.
 __device__ __forceinline__ int chunk_cost(const Kv8AttnParams &p, const ChunkSeq &s, int mb) {
   const int last = min(mb * kChunkRows + kChunkRows, s.rows * p.G) - 1;
-  return max(1, (row_sees(p, row_query(p, last), s.len, s.rows) + 127) / 128);
+  const int tiles = max(1, (row_sees(p, row_query(p, last), s.len, s.rows) + 127) / 128);
+  return p.pair ? (tiles + 1) / 2 : tiles;
 }
 // A head's units together: by one thread, or by a warp.
 __device__ __forceinline__ long long chunk_seq_cost(const Kv8AttnParams &p, int b) {
@@ -296,7 +302,7 @@ __device__ __forceinline__ bool chunk_next(ChunkShared &sb, uint32_t x, bool arr
 // factors.  One body for both warps: the code streams of an SM's roles share its
 // instruction fetch, which bounds this kernel when they are long.  Page numbers and exponents are fetched 32 pages at a time, one batch
 // ahead of their use.
-template <int D>
+template <int D, bool kPair>
 __device__ __forceinline__ void chunk_load(const Kv8AttnParams &p, bool kV, const CUtensorMap *map,
                                            ChunkShared &sb, uint8_t *ring, int lane,
                                            volatile int *abort_flag) {
@@ -318,10 +324,11 @@ __device__ __forceinline__ void chunk_load(const Kv8AttnParams &p, bool kV, cons
       break;
     }
     if (sg.mb < 0) break;
+    const int first = kPair ? 2 * sg.j0 : sg.j0, n = kPair ? 2 * sg.n : sg.n;  // key tiles
     // lane's page of the batch that starts at tile x of the segment, or -1
     auto fetch = [&](int x) -> int {
-      const long long t = (long long)(sg.j0 + x) * 128 + ((long long)lane << p.page_log2);
-      if (x >= sg.n || t >= sg.len || t >= (long long)(sg.j0 + sg.n) * 128) return -1;
+      const long long t = (long long)(first + x) * 128 + ((long long)lane << p.page_log2);
+      if (x >= n || t >= sg.len || t >= (long long)(first + n) * 128) return -1;
       const int id = p.table[kv8_table_offset(g, sg.b, (int)(t >> p.page_log2))];
       if (kv8_page_ok(g, id)) return id;
       if (!kV) atomicCAS(p.err, 0, kDevErrIndex);
@@ -333,7 +340,7 @@ __device__ __forceinline__ void chunk_load(const Kv8AttnParams &p, bool kV, cons
     int id = fetch(0), ex = fetch_exp(id);
     int id_next = fetch(batch), ex_next = 0;
 #pragma unroll 1
-    for (int j = 0; j < sg.n; ++j, ++idx) {
+    for (int j = 0; j < n; ++j, ++idx) {
       const int x = j & (batch - 1);  // tile of the batch
       if (x == 0 && j > 0) {
         id = id_next;
@@ -386,7 +393,7 @@ __device__ __forceinline__ void chunk_load(const Kv8AttnParams &p, bool kV, cons
   }
 }
 
-template <int D>
+template <int D, bool kPair>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     tk_kv8_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
@@ -494,7 +501,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         step0 += sg.n;
         continue;
       }
-      const int first = sg.mb * kChunkRows + t * 128;
+      const int first = kPair ? 0 : sg.mb * kChunkRows + t * 128;
       const int r_end = sg.rows * p.G;
       const int k_base = sg.j0 * 128, step_end = step0 + sg.n;
       const float c =
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           goto done;
         }
         s_phase ^= 1;
-        const uint32_t idx = step0 + j;
+        const uint32_t idx = kPair ? 2 * (step0 + j) + t : step0 + j;  // key tiles before
         if (idle) {
           if (!mbar_wait(&sb.v_ready[idx % C::kV16s], (idx / C::kV16s) & 1, abort_flag)) {
             chunk_abort(sb, p.err);
@@ -553,7 +560,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 128; ++i) reg_barrier(s[i]);
-        const int k0 = k_base + j * 128;
+        const int k0 = kPair ? 2 * (k_base + j * 128) + t * 128 : k_base + j * 128;
         if (k0 + 128 > vis_min || valid != 0xff) {
           const int lim = vis - k0;
 #pragma unroll
@@ -679,7 +686,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         goto done;
       }
       const bool have = sg.mb >= 0;
-      const int n = have ? sg.n : 0;
+      const int n = have ? (kPair ? 2 * sg.n : sg.n) : 0;  // key tiles
+      const int first = kPair ? 2 * sg.j0 : sg.j0;
       int e_run = 0, e_max = kKv8ExpMin, e_t0 = 0, e_t1 = 0;
 #pragma unroll 1
       for (int j = 0; j <= n; ++j) {
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (l == 0.f) oscale = 0.f;  // no position seen (O is 0)
             const float lse =
                 l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994531f;
-            const int r = pmb * kChunkRows + t * 128 + row;
+            const int r = kPair ? row : pmb * kChunkRows + t * 128 + row;
             const bool ok = r < prows * p.G;
             const int i = ok ? row_query(p, r) : 0;
             const int see = ok ? row_sees(p, i, plen, prows) : 0;
@@ -781,7 +789,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           goto done;
         }
         const int v_valid = sb.v_valid[idx & 7];
-        const int k0 = (sg.j0 + j) * 128;
+        const int k0 = (first + j) * 128;
         {
           // (runs that could not be read carry the least exponent)
           int e8 = sb.v_exp8[idx & 7][lane & 7];
@@ -858,8 +866,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           mbar_arrive(&sb.v_ready[ws]);
           mbar_arrive(&sb.v_empty[vs]);
         }
-        if (j == sg.n0 - 1) e_t0 = e_run;
-        if (j == sg.n1 - 1) e_t1 = e_run;
+        if (j == (kPair ? n - 2 : sg.n0 - 1)) e_t0 = e_run;
+        if (j == (kPair ? n - 1 : sg.n1 - 1)) e_t1 = e_run;
       }
       if (!have) break;
       __syncwarp();
@@ -938,7 +946,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             tc_fence_after_sync();
             if (do_pv) {
-              const uint32_t v_lo = v_lo0 + ws * (C::kV16 >> 4);
+              const uint32_t v_lo = v_lo0 + (kPair ? t : ws) * (C::kV16 >> 4);
               umma_ts_w_rt(tO, tS, v_lo, hi128, idO, j > 1 ? 1u : 0u);
 #pragma unroll
               for (int kk = 1; kk < 8; ++kk)
@@ -957,22 +965,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               }
               umma_commit(&sb.s_full[t]);
             }
+            if constexpr (kPair) {  // each tile has its own key and value tiles
+              if (do_pv) umma_commit(&sb.v_free[t]);
+              if (do_s) {
+                umma_commit(&sb.k_empty[ks]);
+                k_ready = false;
+                if (++ks == C::kKs) {
+                  ks = 0;
+                  k_turn ^= 1;
+                }
+              }
+            }
             if (do_pv && j == n_t) {
               umma_commit(&sb.o_full[t]);
               parts ^= 1u << t;
               started |= 1u << t;
             }
           }
-          if (j < n) {
-            umma_commit(&sb.k_empty[ks]);
-            if (++ks == C::kKs) {
-              ks = 0;
-              k_turn ^= 1;
+          if constexpr (!kPair) {
+            if (j < n) {
+              umma_commit(&sb.k_empty[ks]);
+              if (++ks == C::kKs) {
+                ks = 0;
+                k_turn ^= 1;
+              }
             }
-          }
-          if (j >= 1) {
-            umma_commit(&sb.v_free[ws]);
-            ws ^= 1;
+            if (j >= 1) {
+              umma_commit(&sb.v_free[ws]);
+              ws ^= 1;
+            }
           }
         }
       }
@@ -1030,9 +1051,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           mbar_arrive(&sb.seg_full[x & 3]);
           break;
         }
-        const int t0 = chunk_tiles(p, mb * kChunkRows, q.len, q.rows);
-        const int t1 = chunk_tiles(p, mb * kChunkRows + 128, q.len, q.rows);
-        const int cost = max(t0, t1);
+        const int cost = chunk_cost(p, q, mb);
+        const int t0 = kPair ? cost : chunk_tiles(p, mb * kChunkRows, q.len, q.rows);
+        const int t1 = kPair ? cost : chunk_tiles(p, mb * kChunkRows + 128, q.len, q.rows);
         const int n = (int)min((long long)(cost - j), left);
         sg.b = b;
         sg.h = h;
@@ -1043,7 +1064,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         sg.n1 = min(max(t1 - j, 0), n);
         sg.len = q.len;
         sg.rows = q.rows;
-        sg.whole = j == 0 && n == cost;
+        sg.whole = !kPair && j == 0 && n == cost;
         mbar_arrive(&sb.seg_full[x & 3]);
         left -= n;
         j += n;
@@ -1064,7 +1085,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     if (warp == 13 || warp == 14)
-      chunk_load<D>(p, warp == 13, warp == 13 ? &tm_v : &tm_k, sb,
+      chunk_load<D, kPair>(p, warp == 13, warp == 13 ? &tm_v : &tm_k, sb,
                     smem + (warp == 13 ? C::kOffV : C::kOffK), lane, abort_flag);
   }
 done:
@@ -1077,30 +1098,36 @@ done:
   }
 }
 
-// Where a unit's partials lie: runs [c0, c1], of which c0's is its slot `first`;
-// c0 == c1: one run held the unit whole.  `before` and `all`: steps of the
-// head's units before unit mb, and of all of them (after grid_wait).
+// Where a row's partials lie: n of them (0: one run held the unit whole), from
+// run c0 on, c0's in its slot `first`; with pairs two a run.  `before` and `all`:
+// steps of the head's units before the row's, and of all of them (after grid_wait).
 struct ChunkParts {
-  int c0, c1, first;
+  int c0, n, first, pair;
+  __device__ __forceinline__ size_t row(int k, int r) const {  // of the partials' rows
+    const int c = pair ? k >> 1 : k;
+    return ((size_t)(c0 + c) * 2 + (c == 0 ? first : 0)) * kChunkRows + r % kChunkRows +
+           (pair ? (k & 1) * 128 : 0);
+  }
 };
 __device__ __forceinline__ ChunkParts chunk_parts(const Kv8AttnParams &p, const ChunkSeq &s, int b,
-                                                  int h, int mb, int tile_first, long long before,
+                                                  int h, int r, long long before,
                                                   long long all) {
   const long long share = p.prefix[p.B];
   const long long s0 = p.prefix[b] + h * all + before;
-  ChunkParts r;
-  r.c0 = (int)(s0 / share);
-  r.c1 = (int)((s0 + chunk_cost(p, s, mb) - 1) / share);
-  r.first = r.c0 * share == s0 ? 0 : 1;
-  // runs that hold no key tile of the row's tile wrote nothing for it
-  if (r.c0 != r.c1) {
-    const int tiles = chunk_tiles(p, tile_first, s.len, s.rows);
-    const int end = (int)((s0 + tiles - 1) / share);
-    // (all in the first run: still a partial, joined alone)
-    r.c1 = end < r.c1 ? end : r.c1;
-    if (r.c1 == r.c0) r.c1 = -1 - r.c0;
+  ChunkParts a;
+  a.pair = p.pair;
+  a.c0 = (int)(s0 / share);
+  a.first = a.c0 * share == s0 ? 0 : 1;
+  const int c1 = (int)((s0 + chunk_cost(p, s, r / kChunkRows) - 1) / share);
+  if (p.pair) {
+    a.n = 2 * (c1 - a.c0 + 1);
+  } else if (c1 == a.c0) {
+    a.n = 0;
+  } else {  // runs that hold no key tile of the row's tile wrote nothing for it
+    const int tiles = chunk_tiles(p, r / 128 * 128, s.len, s.rows);
+    a.n = min(c1, (int)((s0 + tiles - 1) / share)) - a.c0 + 1;
   }
-  return r;
+  return a;
 }
 
 // Steps of a head's units before unit mb, and of all: a warp.
@@ -1131,12 +1158,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   chunk_before(p, s, mb, threadIdx.x & 31, before, all);
   grid_wait();  // (above: only what the launch before leaves alone)
   if (r >= s.rows * p.G) return;
-  const ChunkParts c = chunk_parts(p, s, b, h, mb, r / 128 * 128, before, all);
-  if (c.c0 == c.c1) return;
+  const ChunkParts at = chunk_parts(p, s, b, h, r, before, all);
+  if (at.n == 0) return;
   const int i = row_query(p, r);
   const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
-  merge_row<D>(p.part + (size_t)(r % kChunkRows) * (D + 4), (size_t)kChunkRows * (D + 4), c.c0,
-               c.c1 < 0 ? c.c0 : c.c1, c.first, p.o + orow * D, p.lse + orow);
+  merge_row<D>([&](int k) { return p.part + at.row(k, r) * (D + 4); }, at.n, p.o + orow * D,
+               p.lse + orow);
 }
 
 // Merge where units lie in few runs: a warp takes four rows of one tile, all
@@ -1155,11 +1182,8 @@ __global__ void __launch_bounds__(256)
   chunk_before(p, s, mb, lane, before, all);
   grid_wait();  // (above: only what the launch before leaves alone)
   if (r0 >= r_end) return;
-  const ChunkParts at = chunk_parts(p, s, b, h, mb, r0 / 128 * 128, before, all);
-  if (at.c0 == at.c1) return;
-  const int c_end = at.c1 < 0 ? at.c0 : at.c1;
-  const size_t slot = (size_t)kChunkRows * (D + 4);
-  const float *base = p.part + (size_t)(r0 % kChunkRows) * (D + 4);
+  const ChunkParts at = chunk_parts(p, s, b, h, r0, before, all);
+  if (at.n == 0) return;
   float mx[kChunkMergeRows], z[kChunkMergeRows], acc[kChunkMergeRows][kPer];
 #pragma unroll
   for (int i = 0; i < kChunkMergeRows; ++i) {
@@ -1169,8 +1193,8 @@ __global__ void __launch_bounds__(256)
     for (int k = 0; k < kPer; ++k) acc[i][k] = 0.f;
   }
 #pragma unroll 2
-  for (int c = at.c0; c <= c_end; ++c) {
-    const float *d = base + ((size_t)c * 2 + (c == at.c0 ? at.first : 0)) * slot;
+  for (int c = 0; c < at.n; ++c) {
+    const float *d = p.part + at.row(c, r0) * (D + 4);
     float l[kChunkMergeRows], x[kChunkMergeRows][kPer];
 #pragma unroll
     for (int i = 0; i < kChunkMergeRows; ++i) {

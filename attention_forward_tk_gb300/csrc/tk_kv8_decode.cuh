@@ -73,6 +73,7 @@ struct Kv8AttnParams {
   int causal;
   float scale_log2;  // scale * log2(e)
   int tile_rows;     // (few rows) a tile's rows, at least Nq * G
+  int pair;          // (many rows) the two tiles of a unit share its rows
   int ctas;          // runs the work is cut into
   int *err;
   float *part;       // [ctas, 2, rows of a tile or unit, D + 4]
@@ -802,13 +803,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
   }
 }
 
-// One row's partials [c0, c1] joined by a block: a warp takes every eighth, its
-// lanes D/32 columns each; then the warps.  A partial is O relative to 2^M, with
-// m, M and l behind it (all relative to the same row's); c0's is at `first`.
+// One row's n partials joined by a block: a warp takes every eighth, its lanes
+// D/32 columns each; then the warps.  at(i): partial i, O relative to 2^M with
+// m, M and l behind it.
 constexpr int kMergeWarps = 8;
-template <int D>
-__device__ __forceinline__ void merge_row(const float *base, size_t slot, int c0, int c1,
-                                          int first, __nv_bfloat16 *o, float *lse) {
+template <int D, typename At>
+__device__ __forceinline__ void merge_row(At at, int n, __nv_bfloat16 *o, float *lse) {
   constexpr int kPer = D / 32;
   __shared__ float stat[kMergeWarps][3];
   __shared__ float cols[kMergeWarps][D];
@@ -818,15 +818,15 @@ __device__ __forceinline__ void merge_row(const float *base, size_t slot, int c0
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
   constexpr int kDeep = 4;  // partials in flight
 #pragma unroll 1
-  for (int c = c0 + warp; c <= c1; c += kMergeWarps * kDeep) {
+  for (int c = warp; c < n; c += kMergeWarps * kDeep) {
     float4 st[kDeep];
     float x[kDeep][kPer];
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
       const int ci = c + i * kMergeWarps;
       st[i] = make_float4(kDecNone, kDecNone, 0.f, 0.f);
-      if (ci <= c1) {
-        const float *d = base + ((size_t)ci * 2 + (ci == c0 ? first : 0)) * slot;
+      if (ci < n) {
+        const float *d = at(ci);
         st[i] = *reinterpret_cast<const float4 *>(d + D);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) x[i][k] = d[lane * kPer + k];
@@ -931,7 +931,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (r >= rows * p.G || c0 == c1) return;
   const int i = row_query(p, r);
   const long long orow = ((long long)b * p.H + h * p.G + (r - i * p.G)) * p.Nq + i;
-  merge_row<D>(base, slot, c0, c1, first0, p.o + orow * D, p.lse + orow);
+  merge_row<D>(
+      [&](int k) { return base + ((size_t)(c0 + k) * 2 + (k == 0 ? first0 : 0)) * slot; },
+      c1 - c0 + 1, p.o + orow * D, p.lse + orow);
 }
 
 }  // namespace tkattn
