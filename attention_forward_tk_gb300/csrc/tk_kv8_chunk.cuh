@@ -26,9 +26,9 @@
 // the fp32 sum of the unrounded P, the rounding of each tile's largest P
 // carried into the divisor.
 //
-// With at most 128 rows a (sequence, head) (kPair) both tiles hold the same rows
-// and take every other key tile: a step is two key tiles, each tile of a run
-// leaves a partial result, and the softmax of one works beside the other's
+// With at most 128 rows a (sequence, head) at D = 64 (kPair) both tiles hold the same rows
+// and take every other key tile: a step is two key tiles, the tiles' results are
+// joined at the end (or both left as partials), and the softmax of one works beside the other's
 // products as it does with 256 rows.
 //
 // Roles (one CTA an SM, 512 threads):
@@ -716,8 +716,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const float l = sb.l_fin[pc & 1][t][row];
             float oscale = exp2i(-pe[t]) / (l + sb.lc_fin[pc & 1][t][row]);
             if (l == 0.f) oscale = 0.f;  // no position seen (O is 0)
-            const float lse =
-                l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994531f;
+            float m2 = l == 0.f ? -INFINITY : m + lg2_approx(l);  // log2 of the sum
             const int r = kPair ? row : pmb * kChunkRows + t * 128 + row;
             const bool ok = r < prows * p.G;
             const int i = ok ? row_query(p, r) : 0;
@@ -727,6 +726,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ((long long)pb * p.H + ph * p.G + (ok ? r - i * p.G : 0)) * p.Nq + i;
             float *part_row = p.part + (((size_t)blockIdx.x * 2 + (pseg > 0)) * kChunkRows +
                                         t * 128 + row) * (D + 4);
+            // With pairs a whole unit's first tile is left in the slot (free until the
+            // run's last segment), and joined with the second by the same thread.
+            const bool join = kPair && pwhole && t == 1;
+            const bool last = pwhole && (!kPair || t == 1);
+            const float *other = part_row - 128 * (D + 4);
+            float w_other = 0.f;
+            if (join && ok) {
+              const float mo = other[D], mm = fmaxf(mo, m2);
+              const float a0 = other[D + 2] == 0.f ? 0.f : ex2_approx(mo - mm);
+              const float a1 = l == 0.f ? 0.f : ex2_approx(m2 - mm), sum = a0 + a1;
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              oscale *= a1 * inv;
+              w_other = a0 * inv;
+              m2 = sum == 0.f ? -INFINITY : mm + lg2_approx(sum);
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t o[32];
@@ -737,7 +751,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 reg_barrier(o[k]);
                 o[k] = __float_as_uint(__uint_as_float(o[k]) * oscale);
               }
-              if (ok && pwhole) {
+              if (join && ok) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                  const float4 v = *reinterpret_cast<const float4 *>(other + c0 + k);
+                  const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int z = 0; z < 4; ++z)
+                    o[k + z] = __float_as_uint(fmaf(u[z], w_other, __uint_as_float(o[k + z])));
+                }
+              }
+              if (ok && last) {
                 uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + c0);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -754,18 +778,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               }
             }
             if (ok) {
-              if (pwhole) {
-                p.lse[orow] = lse;
-              } else {  // as merge_row takes it: O is normalised, so l is 1 or nothing
-                const float m2 = l == 0.f ? -INFINITY : m + lg2_approx(l);
+              if (last)
+                p.lse[orow] = m2 * 0.69314718055994531f;
+              else  // as merge_row takes it: O is normalised, so l is 1 or nothing
                 *reinterpret_cast<float4 *>(part_row + D) =
                     make_float4(m2, m2 + kDecLift, l == 0.f ? 0.f : m2 == m2 ? 1.f : m2, 0.f);
-              }
               if (nan) {  // columns in which this row sees a NaN
 #pragma unroll 1
                 for (int k = 0; k < D; ++k)
                   if (sb.nan_pos[par][k] < see) {
-                    if (pwhole)
+                    if (last)
                       p.o[orow * D + k] = __ushort_as_bfloat16((unsigned short)0x7fc0u);
                     else
                       part_row[k] = __uint_as_float(0x7fc00000u);
@@ -828,7 +850,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int y = 0; y < 4; ++y) any |= (x[y] & 0x7f7f7f7fu) + 0x01010101u;
           put(tr, pc, x);
         };
-        if constexpr (kPair && D == 64) {
+        if constexpr (kPair) {
+          static_assert(!kPair || D == 64, "one piece of a row a read");
           // Two tiles a step, short rows: all of a lane's reads in flight (110 -> 85 us
           // for 32 sequences of up to 32768 positions, 48 rows a head).
           uint4 w[4];
@@ -1078,7 +1101,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         sg.n1 = min(max(t1 - j, 0), n);
         sg.len = q.len;
         sg.rows = q.rows;
-        sg.whole = !kPair && j == 0 && n == cost;
+        sg.whole = j == 0 && n == cost;
         mbar_arrive(&sb.seg_full[x & 3]);
         left -= n;
         j += n;
@@ -1133,10 +1156,10 @@ __device__ __forceinline__ ChunkParts chunk_parts(const Kv8AttnParams &p, const 
   a.c0 = (int)(s0 / share);
   a.first = a.c0 * share == s0 ? 0 : 1;
   const int c1 = (int)((s0 + chunk_cost(p, s, r / kChunkRows) - 1) / share);
-  if (p.pair) {
-    a.n = 2 * (c1 - a.c0 + 1);
-  } else if (c1 == a.c0) {
+  if (c1 == a.c0) {
     a.n = 0;
+  } else if (p.pair) {
+    a.n = 2 * (c1 - a.c0 + 1);
   } else {  // runs that hold no key tile of the row's tile wrote nothing for it
     const int tiles = chunk_tiles(p, r / 128 * 128, s.len, s.rows);
     a.n = min(c1, (int)((s0 + tiles - 1) / share)) - a.c0 + 1;

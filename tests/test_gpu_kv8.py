@@ -223,6 +223,11 @@ CASES = [
     ([2000, 300], 1, 4, 8, [8, 5], 64, 128, False),
     ([900, 130], 2, 7, 9, None, 16, 64, True),
     ([900, 130], 1, 10, 5, None, 128, 128, True),
+    # runs that hold many short sequences, of every kernel
+    ([33, 300, 1] * 70, 2, 5, 12, None, 128, 64, True),
+    ([33, 300, 1] * 70, 2, 10, 6, None, 16, 128, True),
+    ([33, 300, 7] * 60, 2, 10, 14, None, 32, 128, True),
+    ([33, 300, 1] * 90, 2, 8, 5, None, 32, 64, True),
 ]
 
 
