@@ -66,7 +66,8 @@ int check_geom(const void *k_cache, const void *v_cache, const void *k_exp, cons
   if (page != 16 && page != 32 && page != 64 && page != 128) return TK_ATTN_ERR_UNSUPPORTED;
   if (((uintptr_t)k_cache | (uintptr_t)v_cache) & 15u || (uintptr_t)table & 3u)
     return TK_ATTN_ERR_UNSUPPORTED;
-  if ((long long)max_pages * page > 0x7fffffffLL || 2LL * Hkv > 65535 ||
+  // (positions are rounded up to whole tiles in 32 bits)
+  if ((long long)max_pages * page > 0x7fffff00LL || 2LL * Hkv > 65535 ||
       (long long)num_pages * Hkv * page > 0x7fffffffLL)
     return TK_ATTN_ERR_UNSUPPORTED;
   return TK_ATTN_OK;

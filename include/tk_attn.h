@@ -471,6 +471,10 @@ int tk_attn_qk_norm_rope_bwd_check_args(
  * its range (a page not in [0, num_pages), a length past max_pages * page, a
  * negative count, ...) is skipped or clamped, never followed, and
  * tk_attn_last_device_error then returns TK_ATTN_ERR_BAD_INDEX.
+ *
+ * Limits of all kv8 calls (else TK_ATTN_ERR_UNSUPPORTED): D 64 or 128; B at
+ * most 65535, Hkv 32767; max_pages * page at most 2^31 - 256; num_pages * Hkv *
+ * page below 2^31.
  */
 
 /*
@@ -539,7 +543,11 @@ int tk_attn_kv8_read_check_args(const void *k_cache, const void *v_cache, const 
  *
  * A row with no visible position gets o = 0 and lse = -inf.  Positions in a
  * page out of range count as masked.  What lies in masked positions, NaN codes
- * among it, has no effect.  Returns as tk_attn_fwd_splitkv.
+ * among it, has no effect; a NaN a row sees makes its o NaN (a key's: every
+ * column and lse; a value's: that column).  Equal calls on one device give
+ * equal bits.  Also at most Nq * (H / Hkv)^2 < 2^31, B * H < 2^31 and
+ * B * Hkv * (max_pages * page / 64 + 1) <= 2^30 (else TK_ATTN_ERR_UNSUPPORTED).
+ * Two launches.  Returns as tk_attn_fwd_splitkv.
  */
 int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v_cache, const void *k_exp,
                     const void *v_exp, const int *page_table, const int *lengths,

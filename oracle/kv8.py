@@ -88,7 +88,7 @@ def attention(q, k, v, see, scale):
     """One sequence and query head in float64: q [N, D] against k, v [n, D],
     row i seeing the first see[i] positions.  Returns o, lse, and the bounds' parts:
     sum p |v| per output, and how far rounding can move a row's scores (fp32 sums
-    of D terms, and queries held in fp16 relative to their row's largest)."""
+    of D terms, and how the kernels hold the queries)."""
     N, D = q.shape
     o = np.zeros((N, D))
     mag = np.zeros((N, D))
@@ -105,6 +105,14 @@ def attention(q, k, v, see, scale):
         lse[i] = top + np.log(z)
         o[i] = (p / z) @ v[:m]
         mag[i] = (p / z) @ np.abs(v[:m])
-        off[i] = scale * float(np.max(D * 2.0 ** -24 * (np.abs(k[:m]) @ np.abs(q[i])) +
-                                      2.0 ** -25 * np.abs(q[i]).max() * np.abs(k[:m]).sum(1)))
+        top_q = np.abs(q[i]).max()
+        # Queries held in fp16 relative to their largest: off by at most 2^-25 of it.
+        # Held as two E4M3 terms, scaled so that the largest lies in [128, 256): a value
+        # of eight bits is exact while its last bit is at least E4M3's least, 2^-9, so
+        # from 2^-2 on (2^-9 of the largest, at the least); smaller ones are off by half
+        # that step, 2^-10 (2^-17 of the largest).
+        small = np.abs(q[i]) < 2.0 ** -9 * top_q
+        off[i] = scale * float(np.max(
+            D * 2.0 ** -24 * (np.abs(k[:m]) @ np.abs(q[i])) +
+            top_q * (2.0 ** -25 * np.abs(k[:m]).sum(1) + 2.0 ** -17 * np.abs(k[:m]) @ small)))
     return o, lse, mag, off

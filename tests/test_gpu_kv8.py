@@ -4,8 +4,7 @@ Writing and reading back are exact: codes, exponents and bf16 values are
 compared bit for bit.
 
 Bounds of the attention, before any run.  A score is off by `off` (the oracle's:
-fp32 sums of D products, and queries held in fp16 relative to their row's
-largest), so a weight by 2 off relative (its own and the sum's); a weight is rounded to fp16
+fp32 sums of D products, and how the kernels hold the queries), so a weight by 2 off relative (its own and the sum's); a weight is rounded to fp16
 (half a step 2^-11) and the special-function units' 2^x and the fp32 sums add
 less than 2^-16; O is rounded to bf16 (half a step 2^-8):
   |dO| <= 2^-8 |O| + (2^-11 + 2^-16 + 2 off) sum p|v|,
@@ -228,6 +227,11 @@ CASES = [
     ([33, 300, 1] * 70, 2, 10, 6, None, 16, 128, True),
     ([33, 300, 7] * 60, 2, 10, 14, None, 32, 128, True),
     ([33, 300, 1] * 90, 2, 8, 5, None, 32, 64, True),
+    # more sequences than the tensor-core kernel has threads; sequences of many units
+    ([40, 3] * 350, 1, 6, 5, None, 16, 128, True),
+    ([40, 3] * 350, 1, 9, 5, None, 16, 64, False),
+    ([700, 1300], 1, 4, 600, [600, 577], 128, 64, True),
+    ([700, 10, 1300], 1, 3, 900, [600, 0, 900], 64, 128, True),
 ]
 
 
@@ -311,12 +315,15 @@ def test_far_positions_and_shared_pages(tk_lib):
     tk.kv8_write(cache, k.to(DEV), v.to(DEV), one, i32([0]))
     q = torch.randn((1, 4, 1, D), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
     table = torch.full((1, n // page), P - 1, dtype=torch.int32, device=DEV)
-    o, lse = tk.attention_forward_kv8(q.to(DEV), cache, table, i32([n]))
     small = tk.kv8_cache(1, H, page, D, device=DEV)
-    for a, b in zip(small, cache):
-        a.view(torch.uint8)[0] = b.view(torch.uint8)[P - 1]
-    check(q.to(DEV), small, i32([[0]]), [page], None, True, D ** -0.5,
-          o, lse - float(np.log(n // page)))
+    for x, y in zip(small, cache):
+        x.view(torch.uint8)[0] = y.view(torch.uint8)[P - 1]
+    # one query of 4 heads, and 20 of 4 (the tensor core's tiles), all positions visible
+    for Nq in (1, 20):
+        qn = q.expand(1, 4, Nq, D).contiguous().to(DEV)
+        o, lse = tk.attention_forward_kv8(qn, cache, table, i32([n]), causal=False)
+        check(qn, small, i32([[0]]), [page], None, False, D ** -0.5,
+              o, lse - float(np.log(n // page)))
     kk, vv = tk.kv8_read(cache, one, i32([page]), n=page)
     ks, vs = tk.kv8_read(small, i32([[0]]), i32([page]), n=page)
     assert torch.equal(kk, ks) and torch.equal(vv, vs)
@@ -330,9 +337,9 @@ def test_streams_capture_and_workspaces(tk_lib):
     want = tk.attention_forward_kv8(q, cache, table, n)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    for s in (side, side.cuda_stream):
+    for s in (side, side.cuda_stream, 0):
         got = tk.attention_forward_kv8(q, cache, table, n, stream=s)
-        side.synchronize()
+        torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     # a decode step captured once, replayed while the cache grows
     new_k = torch.randn((3, 2, 1, 128), device=DEV).to(torch.bfloat16)

@@ -200,3 +200,48 @@ def test_streams_capture_and_refusals(tk_lib):
         a.update(bad)
         with pytest.raises(ValueError):
             tk.qk_norm_rope_forward(a["q"], a["k"], a["qw"], a["kw"], a["turns"], a["positions"])
+
+
+def test_a_training_step_captured(tk_lib):
+    """Forward and backward in one graph, replayed on new inputs."""
+    B, N, H, Hk, D = 2, 33, 4, 2, 64
+    x = torch.randn((B, N, H + Hk, D), device=DEV).to(torch.bfloat16)
+    qw, kw = weights(D, torch.float32, 2)
+    turns = tk.rope_turns(D)
+    dy = [torch.randn(s, device=DEV).to(torch.bfloat16) for s in ((B, H, N, D), (B, Hk, N, D))]
+
+    def step():
+        leaf = x.detach().requires_grad_()
+        ws = [w.detach().requires_grad_() for w in (qw, kw)]
+        q, k = tk.qk_norm_rope(leaf[:, :, :H].transpose(1, 2), leaf[:, :, H:].transpose(1, 2), *ws,
+                               turns)
+        return (q, k, *torch.autograd.grad((q, k), (leaf, *ws), dy))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (1, 2):
+        x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
+def test_broadcast_gradients(tk_lib):
+    """A gradient expanded over heads and tokens is read where it lies."""
+    B, N, H, Hk, D = 2, 17, 3, 2, 64
+    q, k = fused(B, N, H, Hk, D, 3)
+    qw, kw = weights(D, torch.float32, 5)
+    turns = tk.rope_turns(D)
+    one = torch.randn((B, 1, 1, D), device=DEV).to(torch.bfloat16)
+    dy = [one.expand(t.shape) for t in (q, k)]
+    got = tk.qk_norm_rope_backward(q, k, qw, kw, turns, *dy)
+    want = tk.qk_norm_rope_backward(q, k, qw, kw, turns, *(t.contiguous() for t in dy))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
