@@ -36,7 +36,7 @@
 namespace tkattn {
 namespace {
 
-constexpr int kNrThreads = 256;
+constexpr int kNrFwdThreads = 128, kNrBwdThreads = 256;
 constexpr int kNrFwdHeads = 16, kNrBwdHeads = 8;  // heads a row group takes for one token, at most
 // Rows of partial weight gradients: one for each block of the backward.
 constexpr int kNrBwdMaxBlocks = 2048;
@@ -80,10 +80,17 @@ struct Raw {  // eight bf16 values as loaded
   uint2 lo, hi;
 };
 
+template <bool kHalves>
 __device__ __forceinline__ Raw load8(const __nv_bfloat16 *row, int lo, int hi) {
   Raw r;
-  r.lo = __ldg(reinterpret_cast<const uint2 *>(row + lo));
-  r.hi = __ldg(reinterpret_cast<const uint2 *>(row + hi));
+  if constexpr (kHalves) {
+    r.lo = __ldg(reinterpret_cast<const uint2 *>(row + lo));
+    r.hi = __ldg(reinterpret_cast<const uint2 *>(row + hi));
+  } else {  // eight in a row
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + lo));
+    r.lo = make_uint2(v.x, v.y);
+    r.hi = make_uint2(v.z, v.w);
+  }
   return r;
 }
 
@@ -105,16 +112,16 @@ __device__ __forceinline__ void pairs_of(const Raw &r, float (&a)[4], float (&b)
 template <bool kHalves>
 __device__ __forceinline__ void store8(__nv_bfloat16 *row, int lo, int hi, const float (&a)[4],
                                        const float (&b)[4]) {
-  uint2 x, y;
   if constexpr (kHalves) {
-    x = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-    y = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+    *reinterpret_cast<uint2 *>(row + lo) =
+        make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    *reinterpret_cast<uint2 *>(row + hi) =
+        make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
   } else {
-    x = make_uint2(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]));
-    y = make_uint2(pack_bf16x2(a[2], b[2]), pack_bf16x2(a[3], b[3]));
+    *reinterpret_cast<uint4 *>(row + lo) =
+        make_uint4(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]), pack_bf16x2(a[2], b[2]),
+                   pack_bf16x2(a[3], b[3]));
   }
-  *reinterpret_cast<uint2 *>(row + lo) = x;
-  *reinterpret_cast<uint2 *>(row + hi) = y;
 }
 
 // Column of a lane's value i of the first (a) or second (b) of its pairs.
@@ -157,10 +164,10 @@ __device__ __forceinline__ float group_sum(float s) {
 // grid: (token tiles, or fewer blocks that step over them; runs of hpg heads,
 // the queries' first).  A block takes one token for each of its row groups.
 template <int D, bool kHalves, bool kBwd>
-__global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4)
+__global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads, kBwd ? 3 : 8)
     tk_norm_rope_kernel(const __grid_constant__ NrParams p) {
   constexpr int kLanes = D / 8;
-  constexpr int kGroups = kNrThreads / kLanes;
+  constexpr int kGroups = (kBwd ? kNrBwdThreads : kNrFwdThreads) / kLanes;
   constexpr int kUnroll = kBwd ? 2 : 4;  // heads whose rows are loaded together
   const int l = threadIdx.x % kLanes;
   const int grp = threadIdx.x / kLanes;
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4)
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           x[u].lo = x[u].hi = make_uint2(0, 0);
-          if (h + u < end) x[u] = load8(xrow + u * X.sh, lo, hi);
+          if (h + u < end) x[u] = load8<kHalves>(xrow + u * X.sh, lo, hi);
         }
         xrow += kUnroll * X.sh;
 #pragma unroll
@@ -241,8 +248,8 @@ __global__ void __launch_bounds__(kNrThreads, kBwd ? 3 : 4)
         for (int u = 0; u < kUnroll; ++u) {
           x[u].lo = x[u].hi = y[u].lo = y[u].hi = make_uint2(0, 0);
           if (h + u < end) {
-            x[u] = load8(xrow + u * X.sh, lo, hi);
-            y[u] = load8(grow + u * G.sh, lo, hi);
+            x[u] = load8<kHalves>(xrow + u * X.sh, lo, hi);
+            y[u] = load8<kHalves>(grow + u * G.sh, lo, hi);
           }
         }
         xrow += kUnroll * X.sh;
@@ -445,8 +452,8 @@ void fill(NrParams &p, const Call &c) {
 // Heads a row group takes for one token: fewer until there are blocks for
 // every SM (each run of heads computes the token's sines and cosines again), and
 // more again where the runs would pass the grid's second dimension.
-void split(NrParams &p, int D, int most, int max_runs, long long blocks_wanted) {
-  const int groups = kNrThreads / (D / 8);
+void split(NrParams &p, int D, int threads, int most, int max_runs, long long blocks_wanted) {
+  const int groups = threads / (D / 8);
   p.tiles = (int)(((long long)p.B * p.N + groups - 1) / groups);
   auto runs = [&](int hpg) {
     return ((long long)p.H[0] + hpg - 1) / hpg + ((long long)p.H[1] + hpg - 1) / hpg;
@@ -464,7 +471,7 @@ cudaError_t launch(const NrParams &p, int D, bool halves, dim3 grid, cudaStream_
                                         : tk_norm_rope_kernel<64, false, kBwd>)
                               : (halves ? tk_norm_rope_kernel<128, true, kBwd>
                                         : tk_norm_rope_kernel<128, false, kBwd>);
-  return launch_overlapped(kernel, grid, kNrThreads, 0, s, p);
+  return launch_overlapped(kernel, grid, kBwd ? kNrBwdThreads : kNrFwdThreads, 0, s, p);
 }
 
 }  // namespace
@@ -517,7 +524,7 @@ extern "C" int tk_attn_qk_norm_rope(
     p.yb[i] = (long long)p.H[i] * N * D;
     p.dy[i] = {nullptr, 0, 0, 0};
   }
-  split(p, D, kNrFwdHeads, 65535, 4LL * dv.num_sms);
+  split(p, D, kNrFwdThreads, kNrFwdHeads, 65535, 16LL * dv.num_sms);
   const dim3 grid(p.tiles, p.chunks[0] + p.chunks[1]);
   return launch<false>(p, D, !interleaved, grid, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
@@ -614,7 +621,7 @@ extern "C" int tk_attn_qk_norm_rope_bwd(
   p.dy[1] = {static_cast<const __nv_bfloat16 *>(dk_out), dk_out_strides[0], dk_out_strides[1],
              dk_out_strides[2]};
   // At most three blocks an SM (what is resident), each over several tiles.
-  split(p, D, kNrBwdHeads, kNrBwdMaxBlocks, 3LL * dv.num_sms);
+  split(p, D, kNrBwdThreads, kNrBwdHeads, kNrBwdMaxBlocks, 3LL * dv.num_sms);
   p.dw_part = static_cast<float *>(workspace);
   const int runs = p.chunks[0] + p.chunks[1];
   int cols = 3 * dv.num_sms / runs;
