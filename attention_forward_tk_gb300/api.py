@@ -809,8 +809,10 @@ def _norm_rope_function():
         import torch
 
         def rows(t):  # as the C call reads gradients
-            return t if t.stride(3) == 1 and not any(x % 8 for x in t.stride()[:3]) \
-                else t.contiguous()
+            if t.stride(3) == 1 and t.data_ptr() % 16 == 0 and \
+                    not any(x % 8 for x in t.stride()[:3]):
+                return t
+            return t.clone(memory_format=torch.contiguous_format)
 
         class _NormRope(torch.autograd.Function):
             @staticmethod

@@ -245,3 +245,27 @@ def test_broadcast_gradients(tk_lib):
     want = tk.qk_norm_rope_backward(q, k, qw, kw, turns, *(t.contiguous() for t in dy))
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_gradients_at_odd_addresses(tk_lib):
+    """Gradients that autograd hands on as views no 16-byte load could read."""
+    q, k = (t.contiguous().requires_grad_() for t in fused(1, 5, 2, 1, 64, 6))
+    qw, kw = (w.requires_grad_() for w in weights(64, torch.float32, 7))
+    y = tk.qk_norm_rope(q, k, qw, kw, tk.rope_turns(64))
+    odd = torch.zeros(1, dtype=torch.bfloat16, device=DEV)
+    flat = torch.cat([odd, *(t.flatten() for t in y)])
+    dy = torch.randn(flat.shape, device=DEV).to(torch.bfloat16)
+    got = torch.autograd.grad(flat, (q, k, qw, kw), dy)
+    n = y[0].numel()
+    want = tk.qk_norm_rope_backward(q.detach(), k.detach(), qw.detach(), kw.detach(),
+                                    tk.rope_turns(64), dy[1:1 + n].clone().view_as(y[0]),
+                                    dy[1 + n:].clone().view_as(y[1]))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_flags_that_are_neither(tk_lib):
+    q, k = fused(1, 5, 2, 1, 64, 6)
+    qw, kw = weights(64, torch.float32, 7)
+    with pytest.raises(RuntimeError):
+        tk.qk_norm_rope_forward(q, k, qw, kw, None, interleaved=torch.zeros(2))
