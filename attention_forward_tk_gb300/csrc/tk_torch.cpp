@@ -2,9 +2,9 @@
 //
 // A decoder makes these calls for every layer of every token, and at one token
 // a sequence a kernel takes a few microseconds.  Reading some thirty tensor
-// attributes from Python and marshalling the C call through ctypes took 9 to 17
+// attributes from Python and marshalling the C call through ctypes took 11 to 27 us
 // (GB300's host cores); here the checks, the allocations and the call take 3 to
-// 5.  Every function checks its tensors (ValueError), makes their device
+// 9.  Every function checks its tensors (ValueError), makes their device
 // current, allocates through torch what it is not given, enqueues on torch's
 // current stream of that device through the C ABI, and returns the results, or
 // the C call's status where it is not 0.
@@ -93,6 +93,12 @@ int size32(int64_t x) {
   return (int)x;
 }
 
+int truth(PyObject *o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) throw Refused();  // (its exception is set)
+  return t;
+}
+
 PyObject *wrap2(const Tensor &a, const Tensor &b) {
   PyObject *t = PyTuple_New(2);
   PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(a));
@@ -154,7 +160,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const NormRope c(a);
     const double eps = PyFloat_AsDouble(a[6]);
     if (eps == -1.0 && PyErr_Occurred()) return nullptr;
-    const int inter = PyObject_IsTrue(a[7]);
+    const int inter = truth(a[7]);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
     const Tensor oq = a[8] == Py_None
                           ? make(c.q.sizes(), at::kBFloat16, c.q)
@@ -183,7 +189,7 @@ PyObject *norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const NormRope c(a);
     const double eps = PyFloat_AsDouble(a[6]);
     if (eps == -1.0 && PyErr_Occurred()) return nullptr;
-    const int inter = PyObject_IsTrue(a[7]);
+    const int inter = truth(a[7]);
     const Tensor &gq = want_rows(tensor(a[8], "dq_out"), "dq_out", c.q.sizes(), c.dev);
     const Tensor &gk = want_rows(tensor(a[9], "dk_out"), "dk_out", c.k.sizes(), c.dev);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
@@ -341,13 +347,14 @@ PyObject *kv8_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Kv8 c(a[1], a[2]);
     const Tensor &q = tensor(a[0], "q");
     if (q.dim() != 4 || q.scalar_type() != at::kBFloat16 || !q.is_cuda() || !q.is_contiguous() ||
-        q.get_device() != c.dev || q.size(0) != c.b || q.size(3) != c.D || q.size(1) % c.H)
+        q.get_device() != c.dev || q.size(0) != c.b || q.size(3) != c.D || c.H == 0 ||
+        q.size(1) % c.H)
       refuse(q, "q",
              "a contiguous bfloat16 tensor [B, H, Nq, D] on the cache's device, with the page "
              "table's B, the cache's D and a multiple of its heads");
     const int *lengths = c.per_sequence(a[3], "lengths");
     const int *counts = a[4] == Py_None ? nullptr : c.per_sequence(a[4], "counts");
-    const int causal = PyObject_IsTrue(a[5]);
+    const int causal = truth(a[5]);
     double scale = 1.0 / std::sqrt((double)c.D);
     if (a[6] != Py_None) {
       scale = PyFloat_AsDouble(a[6]);

@@ -232,6 +232,9 @@ CASES = [
     ([40, 3] * 350, 1, 9, 5, None, 16, 64, False),
     ([700, 1300], 1, 4, 600, [600, 577], 128, 64, True),
     ([700, 10, 1300], 1, 3, 900, [600, 0, 900], 64, 128, True),
+    # many rows of few partials each
+    ([300, 900, 64, 1] * 16, 8, 4, 1, None, 64, 128, True),
+    ([300, 900, 0, 65] * 12, 3, 9, 2, [2, 1, 1, 0] * 12, 16, 128, True),
 ]
 
 
@@ -252,6 +255,40 @@ def test_attention(tk_lib, case):
     tk.attention_forward_kv8(q, cache, table, i32(lengths),
                              None if counts is None else i32(counts), causal, out=o2, lse=lse2)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("Nq,G,D", [(1, 4, 128), (2, 8, 128), (5, 8, 64), (7, 9, 64),
+                                    (90, 3, 64), (90, 3, 128)])
+def test_bad_pages_among_good_ones(tk_lib, Nq, G, D):
+    """The positions of a page out of range are masked, wherever it lies."""
+    page, H, lengths = 32, 2, [700, 333, 32]
+    cache, table = make(lengths, H, page, D, seed=5)
+    good = table.clone()
+    bad = {0: [0, 7, 20, 21], 1: [9, 10], 2: [0]}  # (the whole of the last sequence)
+    for b, slots in bad.items():
+        for i, x in enumerate(slots):
+            table[b, x] = (-1, cache.k.shape[0], 2 ** 31 - 1, -2 ** 31)[(b + i) % 4]
+    q = torch.randn((3, H * G, Nq, D), generator=torch.Generator().manual_seed(2))
+    q = q.to(torch.bfloat16).to(DEV)
+    o, lse = tk.attention_forward_kv8(q, cache, table, i32(lengths))
+    assert tk.last_device_error() == tk_lib.TK_ATTN_ERR_BAD_INDEX
+    ck, cv, ke, ve = host(cache)
+    tb = good.cpu().numpy()
+    for b, n in enumerate(lengths):
+        k, v = ref.read(ck, ke, tb, b, n), ref.read(cv, ve, tb, b, n)
+        on = np.array([t // page not in bad[b] for t in range(n)])
+        # the first positions that each row sees, counted among the good ones
+        see = [int(on[:max(0, n - (Nq - 1 - i))].sum()) for i in range(Nq)]
+        for h in range(H * G):
+            wo, wl, mag, off = ref.attention(f64(q)[b, h], k[h // G][on], v[h // G][on], see,
+                                             D ** -0.5)
+            tol = 2.0 ** -8 * np.abs(wo) + (2.0 ** -11 + 2.0 ** -16 + 2 * off[:, None]) * mag
+            assert (np.abs(f64(o)[b, h] - wo) <= tol + 1e-30).all()
+            fin = np.isfinite(wl)
+            got = f64(lse)[b, h]
+            assert np.array_equal(got[~fin], wl[~fin])
+            assert (np.abs(got[fin] - wl[fin]) <=
+                    off[fin] + 2.0 ** -20 * (1 + np.abs(wl[fin]))).all()
 
 
 @pytest.mark.parametrize("Nq,G", [(1, 4), (3, 4), (40, 4)])
@@ -365,6 +402,18 @@ def test_streams_capture_and_workspaces(tk_lib):
         assert start.tolist() == now
         check(q, cache, wide, now, None, True, 128 ** -0.5, *got)
     assert tk.last_device_error() == 0
+
+
+def test_a_cache_without_heads_is_refused(tk_lib):
+    cache = tk.kv8_cache(2, 0, 16, 64, device=DEV)
+    q = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16, device=DEV)
+    table, n = i32([[0, 1]]), i32([1])
+    with pytest.raises(ValueError):
+        tk.attention_forward_kv8(q, cache, table, n)
+    with pytest.raises(tk.TkAttnError):
+        tk.kv8_write(cache, q[:, :0], q[:, :0], table, n)
+    with pytest.raises(tk.TkAttnError):
+        tk.kv8_read(cache, table, n, n=4)
 
 
 def test_refusals(tk_lib):
