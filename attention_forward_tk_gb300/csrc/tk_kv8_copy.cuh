@@ -13,7 +13,14 @@
 //
 // Read: payload -> fp16 (exact) -> fp32, times 2^e (exact), -> bf16 (exact for
 // the exponents a write gives).
-// Both are bound by the bytes they move.
+// Both are bound by the bytes they move.  Measured, with 8 heads of 128: up to
+// 4096 tokens written for each of 8 sequences in 18.5 us (114 MB, 6.1 TB/s); one
+// for each of 64 in 4.1 us, most of it the start of a grid and three dependent
+// reads (position, page, exponent); 8 sequences of up to 16384 positions read
+// back in 72 us (453 MB, 6.3 TB/s).
+// A write's block is a page, not more, because a page's exponent needs all of
+// its new rows; its thread keeps kPage / 128 * D / 8 loads in flight, so a
+// kernel for each page size holds no more registers than its page needs.
 #pragma once
 
 #include <cuda_bf16.h>

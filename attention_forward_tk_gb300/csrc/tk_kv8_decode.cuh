@@ -32,6 +32,14 @@
 //    32 heads.  The 5th-generation path has 128-row tiles, sixteen times the
 //    rows there are.
 //
+// Measured: one query for each of 8 sequences of 16384 positions and 32 heads of
+// 128, 159 us, 6.76 TB/s (the rate of a plain copy); 32 sequences of up to 32768
+// positions, 4 query heads a key head, 164 us, 6.74 TB/s; one sequence of 1000
+// positions 6.0 us, most of it the start of two grids and four dependent reads
+// (length, page, codes, partials).  With 40 rows (5 drafts, 8 heads a key head, D = 64) the
+// products, exponentials and conversions bound it: 33.7 us for what a copy reads
+// in 5.4, the eight warps that an SM's registers hold issuing 40 % of the time.
+//
 // Numbers: q rows are scaled by a power of two to a largest magnitude in
 // [1, 2) before rounding to fp16 (exact but for elements below 2^-14 of the
 // row's largest), the factor returning in the fp32 scores.  m (base 2) is the

