@@ -94,6 +94,7 @@ constexpr int kDecUnit = kDecWarps * 16;  // positions of a unit
 constexpr float kDecTau = 8.f;       // m is exceeded by at most 2^8
 constexpr float kDecLift = 7.f;      // P' is lifted by 2^7
 constexpr float kDecNone = -1e30f;   // references before any score
+constexpr float kDecNoLift = -200.f;  // and what lifts P' then (no value exponent makes it large)
 
 // kNT tiles of eight query rows a warp: up to 40 rows at D = 64 and 24 at
 // D = 128, where the accumulators (kNT * D / 4 a thread) still fit the registers.
@@ -507,10 +508,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       }
     }
     if constexpr (C::kQShared) __syncthreads();
-    // factor of a row of this lane's, and the positions it sees
-    auto factor = [&](int t, int x) -> float {
-      if constexpr (C::kQShared) return q_fac[8 * t + 2 * c4 + x];
-      return f[C::kQShared ? 0 : t][x];
+    // factors of this lane's two rows of a tile, and the positions a row sees
+    auto factors = [&](int t) -> uint64_t {
+      if constexpr (C::kQShared)
+        return *reinterpret_cast<const uint64_t *>(q_fac + 8 * t + 2 * c4);
+      const int i = C::kQShared ? 0 : t;
+      return f2_pack(f[i][0], f[i][1]);
     };
     auto sees = [&](int t, int x) -> int {
       const int r = 8 * t + 2 * c4 + x;
@@ -518,12 +521,13 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
     };
 
     float o[kNT][kSteps][4];
-    float m[kNT][2], mo[kNT][2], l[kNT][2];
+    float nm[kNT][2], dm[kNT][2], l[kNT][2];  // -m; m - M + lift; l
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
-      m[t][0] = m[t][1] = mo[t][0] = mo[t][1] = kDecNone;
+      nm[t][0] = nm[t][1] = -kDecNone;
+      dm[t][0] = dm[t][1] = kDecNoLift;
       l[t][0] = l[t][1] = 0.f;
     }
 
@@ -583,63 +587,73 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
       const bool edge = t0 + 16 > vis_min;
       // z = s - m (log2 units); while no score passes m by more than 2^tau and
       // no m + ve passes M, the references stay and nothing has to be reduced
-      // across the warp.
+      // across the warp.  (Two rows an instruction where there is one.)
+      const uint64_t fk2 = f2_pack(fk, fk), ev2 = f2_pack(ev, ev);
       float z[kNT][4];
-      float top = -INFINITY, up = 0.f;
+      float top = -INFINITY, most = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < kNT; ++t)
+      for (int t = 0; t < kNT; ++t) {
+        const uint64_t fx = f2_mul(factors(t), fk2), nm2 = f2_pack(nm[t][0], nm[t][1]);
+        f2_unpack(f2_fma(f2_pack(s[t][0], s[t][1]), fx, nm2), z[t][0], z[t][1]);
+        f2_unpack(f2_fma(f2_pack(s[t][2], s[t][3]), fx, nm2), z[t][2], z[t][3]);
+        if (edge) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float fx = factor(t, x) * fk;
-          z[t][x] = fmaf(s[t][x], fx, -m[t][x]);
-          z[t][2 + x] = fmaf(s[t][2 + x], fx, -m[t][x]);
-          if (edge) {
+          for (int x = 0; x < 2; ++x) {
             const int see = sees(t, x);
             if (t0 + q8 >= see) z[t][x] = -INFINITY;
             if (t0 + q8 + 8 >= see) z[t][2 + x] = -INFINITY;
           }
-          top = max3(top, z[t][x], z[t][2 + x]);
-          up = fmaxf(up, m[t][x] + ev - mo[t][x]);
         }
-      if (__any_sync(0xffffffffu, top > kDecTau || up > 0.f)) {
+        top = max3(max3(top, z[t][0], z[t][1]), z[t][2], z[t][3]);
+        float d0, d1;
+        f2_unpack(f2_add(f2_pack(dm[t][0], dm[t][1]), ev2), d0, d1);
+        most = max3(most, d0, d1);
+      }
+      if (__any_sync(0xffffffffu, top > kDecTau || most > kDecLift)) {
 #pragma unroll
-        for (int t = 0; t < kNT; ++t)
+        for (int t = 0; t < kNT; ++t) {
+          float fx[2];
+          f2_unpack(f2_mul(factors(t), fk2), fx[0], fx[1]);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float fx = factor(t, x) * fk;
             const bool see0 = z[t][x] != -INFINITY, see1 = z[t][2 + x] != -INFINITY;
-            float mx = fmaxf(see0 ? s[t][x] * fx : -INFINITY, see1 ? s[t][2 + x] * fx : -INFINITY);
+            const float m = -nm[t][x];
+            float mx = fmaxf(see0 ? s[t][x] * fx[x] : -INFINITY,
+                             see1 ? s[t][2 + x] * fx[x] : -INFINITY);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = mx > m[t][x] + kDecTau ? mx : m[t][x];
-            l[t][x] *= ex2_approx(m[t][x] - m_new);
-            m[t][x] = m_new;
-            if (see0) z[t][x] = fmaf(s[t][x], fx, -m_new);
-            if (see1) z[t][2 + x] = fmaf(s[t][2 + x], fx, -m_new);
-            const float mo_new = fmaxf(mo[t][x], m_new + ev);
-            const float up = ex2_approx(mo[t][x] - mo_new);
-            mo[t][x] = mo_new;
+            const float m_new = mx > m + kDecTau ? mx : m;
+            l[t][x] *= ex2_approx(m - m_new);
+            nm[t][x] = -m_new;
+            if (see0) z[t][x] = fmaf(s[t][x], fx[x], -m_new);
+            if (see1) z[t][2 + x] = fmaf(s[t][2 + x], fx[x], -m_new);
+            // M = m - dm + lift: the larger of itself and m + ve
+            const float kept = dm[t][x] + (m_new - m);
+            const float d_new = fminf(kept, kDecLift - ev);
+            const float up = ex2_approx(d_new - kept);
+            dm[t][x] = d_new;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
               o[t][j][x] *= up;
               o[t][j][2 + x] *= up;
             }
           }
+        }
       }
       uint32_t pb[kNT][2];
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
-        float pr[4];
+        // P = 2^(s - m), P' = P 2^(m + ve - M + lift)
+        float d[2], e[4], pr[4];
+        f2_unpack(f2_add(f2_pack(dm[t][0], dm[t][1]), ev2), d[0], d[1]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          // P = 2^(s - m), P' = P 2^(m + ve - M + lift)
-          const float lift = ex2_approx(m[t][x] + ev - mo[t][x] + kDecLift);
-          const float e0 = ex2_approx(z[t][x]), e1 = ex2_approx(z[t][2 + x]);
-          l[t][x] += e0 + e1;
-          pr[x] = e0 * lift;
-          pr[2 + x] = e1 * lift;
-        }
+        for (int x = 0; x < 4; ++x) e[x] = ex2_approx(z[t][x]);
+        const uint64_t lift = f2_pack(ex2_approx(d[0]), ex2_approx(d[1]));
+        const uint64_t e01 = f2_pack(e[0], e[1]), e23 = f2_pack(e[2], e[3]);
+        f2_unpack(f2_add(f2_pack(l[t][0], l[t][1]), f2_add(e01, e23)), l[t][0], l[t][1]);
+        f2_unpack(f2_mul(e01, lift), pr[0], pr[1]);
+        f2_unpack(f2_mul(e23, lift), pr[2], pr[3]);
         // as the 8-wide operand: positions 2 c4, 2 c4 + 1 (and + 8) of row q8
         pb[t][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
         pb[t][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
@@ -743,7 +757,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, kNT>::kCtasPerSm)
           const int row = warp * C::kMergeRows + 8 * (t - tj) + 2 * c4 + x;
           if (q8 == 0)
             *reinterpret_cast<float4 *>(merge_s + row * 4) =
-                make_float4(m[t][x], mo[t][x], ls, 0.f);
+                make_float4(-nm[t][x], kDecLift - dm[t][x] - nm[t][x], ls, 0.f);
           float *d = merge_o + row * C::kRowStride + q8 * C::kRunStride;
 #pragma unroll
           for (int j = 0; j < kSteps; j += 2)
