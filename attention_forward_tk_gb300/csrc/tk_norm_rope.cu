@@ -26,7 +26,7 @@
 // TB/s).  What an SM needs is loads outstanding while other rows are reduced: 32
 // warps with four rows each (64 registers; in blocks of 128 threads, 62 us in
 // blocks of 256).  16 x 1024 tokens of 16 + 16 heads of 64,
-// forward and gradients, take 65 us: 23 + 41, 5.1 TB/s over the five tensors of
+// forward and gradients, take 63 us: 23 + 40, 5.3 TB/s over the five tensors of
 // 67 MB that the two calls read and write.  One token for each of 8 sequences takes 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -44,6 +44,14 @@ namespace tkattn {
 namespace {
 
 constexpr int kNrFwdThreads = 128, kNrBwdThreads = 256;
+// Backward: blocks of an SM, and heads whose rows are loaded together.  With 16-byte
+// loads (neighbours paired) fewer warps with more rows each are the faster (16 x
+// 1024 tokens, 32 heads of 64, with the forward: 63.3 us, 65.3 the other way),
+// with 8-byte loads more warps (4 x 4096, 40 heads of 128: 153 us, 159).
+template <bool kHalves>
+constexpr int kNrBwdBlocks = kHalves ? 3 : 2;
+template <bool kHalves>
+constexpr int kNrBwdUnroll = kHalves ? 2 : 4;
 constexpr int kNrFwdHeads = 16, kNrBwdHeads = 8;  // heads a row group takes for one token, at most
 // Rows of partial weight gradients: one for each block of the backward.
 constexpr int kNrBwdMaxBlocks = 2048;
@@ -171,11 +179,12 @@ __device__ __forceinline__ float group_sum(float s) {
 // grid: (token tiles, or fewer blocks that step over them; runs of hpg heads,
 // the queries' first).  A block takes one token for each of its row groups.
 template <int D, bool kHalves, bool kBwd>
-__global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads, kBwd ? 3 : 8)
+__global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads,
+                                  kBwd ? kNrBwdBlocks<kHalves> : 8)
     tk_norm_rope_kernel(const __grid_constant__ NrParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = (kBwd ? kNrBwdThreads : kNrFwdThreads) / kLanes;
-  constexpr int kUnroll = kBwd ? 2 : 4;  // heads whose rows are loaded together
+  constexpr int kUnroll = kBwd ? kNrBwdUnroll<kHalves> : 4;  // heads whose rows are loaded together
   const int l = threadIdx.x % kLanes;
   const int grp = threadIdx.x / kLanes;
   int lo, hi;
@@ -627,11 +636,12 @@ extern "C" int tk_attn_qk_norm_rope_bwd(
              dq_out_strides[2]};
   p.dy[1] = {static_cast<const __nv_bfloat16 *>(dk_out), dk_out_strides[0], dk_out_strides[1],
              dk_out_strides[2]};
-  // At most three blocks an SM (what is resident), each over several tiles.
-  split(p, D, kNrBwdThreads, kNrBwdHeads, kNrBwdMaxBlocks, 3LL * dv.num_sms);
+  // As many blocks as are resident at once, each over several tiles.
+  const int blocks = (interleaved ? kNrBwdBlocks<false> : kNrBwdBlocks<true>) * dv.num_sms;
+  split(p, D, kNrBwdThreads, kNrBwdHeads, kNrBwdMaxBlocks, blocks);
   p.dw_part = static_cast<float *>(workspace);
   const int runs = p.chunks[0] + p.chunks[1];
-  int cols = 3 * dv.num_sms / runs;
+  int cols = blocks / runs;
   cols = cols < 1 ? 1 : cols > p.tiles ? p.tiles : cols;
   if ((long long)cols * runs > kNrBwdMaxBlocks) cols = kNrBwdMaxBlocks / runs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
