@@ -48,8 +48,8 @@ int kv8_device(DeviceView *dv) {
   Kv8Device &d = g_kv8_dev[dv->index];
   std::call_once(d.once, [&d] {
     d.ok = configure_decode<64, 1>() && configure_decode<64, 2>() && configure_decode<64, 3>() &&
-           configure_decode<64, 5>() && configure_decode<128, 1>() && configure_decode<128, 2>() &&
-           configure_decode<128, 3>() &&
+           configure_decode<64, 4>() && configure_decode<64, 5>() && configure_decode<128, 1>() &&
+           configure_decode<128, 2>() && configure_decode<128, 3>() &&
            configure_chunk<64, false>() && configure_chunk<64, true>() &&
            configure_chunk<128, false>();
   });
@@ -249,11 +249,12 @@ namespace {
 
 // Tiles of eight query rows that a warp of the streaming kernel holds for a
 // call's Nq * G rows, or 0 where the rows go to the 128-row tiles of the tensor
-// core: past 24 rows at D = 128 and 40 at D = 64 the registers spill.
+// core: past 24 rows at D = 128 and 40 at D = 64 the registers spill.  (32 sequences
+// of up to 32768 positions, 2 key heads of 64: 8 to 40 rows in steps of 8 take 33, 43, 50,
+// 68 and 82 us, 48 and 64 rows on the tensor core 90 and 92.)
 int row_tiles(int G, int Nq, int D) {
   const long long tiles = ((long long)Nq * G + 7) / 8;
-  if (tiles <= 3) return (int)tiles;
-  return D == 64 && tiles <= 5 ? 5 : 0;
+  return tiles <= (D == 64 ? 5 : 3) ? (int)tiles : 0;
 }
 // Runs the work is cut into: the CTAs that fit on the device at once.
 int run_count(const DeviceView &dv, int tiles, int D) {
@@ -418,6 +419,7 @@ extern "C" int tk_attn_fwd_kv8(const void *q, const void *k_cache, const void *v
       case 1: e = launch_decode<64, 1>(p, s); break;
       case 2: e = launch_decode<64, 2>(p, s); break;
       case 3: e = launch_decode<64, 3>(p, s); break;
+      case 4: e = launch_decode<64, 4>(p, s); break;
       default: e = launch_decode<64, 5>(p, s); break;
     }
   } else {
