@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   kv8_scan(
       p, [&](int b) { return (by_warp ? sums[b] : chunk_seq_cost(p, b)) * p.g.Hkv; }, blockIdx.x,
       &sb.place, sb.red, blockIdx.x == 0 ? p.prefix : nullptr);
+  if (by_warp) fence_proxy_async_smem();  // the sums are read before a copy lands over them
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
