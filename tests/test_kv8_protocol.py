@@ -186,9 +186,19 @@ def chunk_roles(sim, segs, pair=False, KS=3, VS=2, drop=()):
             step0 += n
         yield from segment("mma", len(segs))
 
-    return {"poster": poster(), "load_k": loader("load_k", False),
-            "load_v": loader("load_v", True), "softmax0": softmax(0), "softmax1": softmax(1),
-            "mma": mma(), **{c: converter(c) for c in conv}}
+    roles = {"poster": poster(), "load_k": loader("load_k", False),
+             "load_v": loader("load_v", True), "softmax0": softmax(0), "softmax1": softmax(1),
+             "mma": mma(), **{c: converter(c) for c in conv}}
+    return {name: by_parity(role) for name, role in roles.items()}
+
+
+def by_parity(role):
+    """A wait sees a phase's parity: the phase before it has to be over already, or
+    the one before that would pass for it."""
+    for op in role:
+        if op[0] == "wait" and op[2] > 0:
+            yield ("check", op[1], op[2] - 1)
+        yield op
 
 
 RUNS = [
