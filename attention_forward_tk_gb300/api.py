@@ -839,7 +839,10 @@ def _norm_rope_function():
 def qk_norm_rope(q, k, q_weight, k_weight, turns, positions=None, eps: float = 1e-6,
                  interleaved: bool = False):
     """Differentiable qk_norm_rope_forward (torch autograd: gradients of q, k
-    and both weights).  Runs on torch's current stream of q's device."""
+    and both weights).  Runs on torch's current stream of q's device.  A backward
+    pass captured into a CUDA graph needs its leaves' graphs built inside the
+    capture: with an eager graph of the same leaves alive, torch accumulates their
+    gradients on that graph's stream, outside the capture."""
     return _norm_rope_function().apply(q, k, q_weight, k_weight, turns, positions, float(eps),
                                        bool(interleaved))
 

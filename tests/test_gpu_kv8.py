@@ -235,6 +235,11 @@ CASES = [
     # many rows of few partials each
     ([300, 900, 64, 1] * 16, 8, 4, 1, None, 64, 128, True),
     ([300, 900, 0, 65] * 12, 3, 9, 2, [2, 1, 1, 0] * 12, 16, 128, True),
+    # calls without a query or without a position
+    ([100, 50], 2, 4, 2, [0, 0], 16, 128, True),
+    ([100, 50], 2, 4, 90, [0, 0], 64, 64, True),
+    ([0, 0], 1, 32, 3, None, 32, 64, False),
+    ([0, 0], 2, 4, 300, None, 32, 128, True),
 ]
 
 
