@@ -180,6 +180,7 @@ extern "C" int tk_attn_kv8_write(const void *k, const long long *k_strides, cons
   p.N = N;
   p.err = dv.err_word;
   const dim3 grid(kv8_span(N, page), 2 * Hkv, B);
+  p.early = one_wave((long long)grid.x * grid.y * grid.z, dv.num_sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = page == 16   ? launch_write<16>(p, D, grid, s)
                         : page == 32 ? launch_write<32>(p, D, grid, s)
@@ -237,6 +238,7 @@ extern "C" int tk_attn_kv8_read(const void *k_cache, const void *v_cache, const 
   p.N = N;
   p.err = dv.err_word;
   const dim3 grid((int)(((long long)N + 63) / 64), 2 * Hkv, B);
+  p.early = one_wave((long long)grid.x * grid.y * grid.z, dv.num_sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
       launch_overlapped(D == 64 ? tk_kv8_read_kernel<64> : tk_kv8_read_kernel<128>, grid,

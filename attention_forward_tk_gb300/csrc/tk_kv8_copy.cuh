@@ -14,8 +14,8 @@
 // Read: payload -> fp16 (exact) -> fp32, times 2^e (exact), -> bf16 (exact for
 // the exponents a write gives).
 // Both are bound by the bytes they move.  Measured, with 8 heads of 128: up to
-// 4096 tokens written for each of 8 sequences in 18.5 us (114 MB, 6.1 TB/s); one
-// for each of 64 in 4.1 us, most of it the start of a grid and three dependent
+// 4096 tokens written for each of 8 sequences in 18.6 us (114 MB, 6.1 TB/s); one
+// for each of 64 in 3.9 us, most of it the start of a grid and three dependent
 // reads (position, page, exponent); 8 sequences of up to 16384 positions read
 // back in 72 us (453 MB, 6.3 TB/s).
 // A write's block is a page, not more, because a page's exponent needs all of
@@ -44,6 +44,7 @@ struct Kv8WriteParams {
   int8_t *exps[2];
   const int *table, *start, *counts;  // counts may be null (every row counts)
   int B, N;
+  int early;  // the next grid may begin beside this one (tk_launch.cuh)
   int *err;
 };
 
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kKv8Threads)
   const int b = blockIdx.z;
   const int which = blockIdx.y >= g.Hkv;
   const int h = blockIdx.y - (which ? g.Hkv : 0);
-  grid_launch_dependents();
+  grid_launch_dependents_if(p.early);
   grid_wait();
   bool bad = false;
   const int start = p.start[b];
@@ -175,16 +176,25 @@ __global__ void __launch_bounds__(kKv8Threads)
     // rows that stay, onto the new grid
     const float s = exp2i(max(held - e, -126));
     uint2 *old = reinterpret_cast<uint2 *>(page);
-    for (int c = threadIdx.x; c < r0 * kVec; c += kKv8Threads) {
-      uint2 w = old[c];
-      uint32_t *q = reinterpret_cast<uint32_t *>(&w);
+    constexpr int kDeep = kMaxVec < 8 ? kMaxVec : 8;  // reads in flight
+#pragma unroll 1
+    for (int c0 = threadIdx.x; c0 < r0 * kVec; c0 += kDeep * kKv8Threads) {
+      uint2 w[kDeep];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 a = e4m3x2_to_float2((uint16_t)(q[i] & 0xffffu));
-        const float2 c2 = e4m3x2_to_float2((uint16_t)(q[i] >> 16));
-        q[i] = pack_e4m3x2(a.x * s, a.y * s) | pack_e4m3x2(c2.x * s, c2.y * s) << 16;
+      for (int u = 0; u < kDeep; ++u)
+        if (c0 + u * kKv8Threads < r0 * kVec) w[u] = old[c0 + u * kKv8Threads];
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        if (c0 + u * kKv8Threads >= r0 * kVec) break;
+        uint32_t *q = reinterpret_cast<uint32_t *>(&w[u]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 a = e4m3x2_to_float2((uint16_t)(q[i] & 0xffffu));
+          const float2 c2 = e4m3x2_to_float2((uint16_t)(q[i] >> 16));
+          q[i] = pack_e4m3x2(a.x * s, a.y * s) | pack_e4m3x2(c2.x * s, c2.y * s) << 16;
+        }
+        old[c0 + u * kKv8Threads] = w[u];
       }
-      old[c] = w;
     }
   }
   const float s = exp2i(max(-e, -126));
@@ -212,6 +222,7 @@ struct Kv8ReadParams {
   const int *table, *lengths;
   __nv_bfloat16 *dst[2];  // [B, Hkv, N, D]
   int B, N;
+  int early;  // the next grid may begin beside this one (tk_launch.cuh)
   int *err;
 };
 
@@ -225,7 +236,7 @@ __global__ void __launch_bounds__(kKv8Threads)
   const int b = blockIdx.z;
   const int which = blockIdx.y >= g.Hkv;
   const int h = blockIdx.y - (which ? g.Hkv : 0);
-  grid_launch_dependents();
+  grid_launch_dependents_if(p.early);
   grid_wait();
   bool bad = false;
   const int len = kv8_length(g, p.lengths[b], &bad);

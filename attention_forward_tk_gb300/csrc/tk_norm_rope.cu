@@ -22,12 +22,12 @@
 // of consecutive rows of a head-major output.
 // Everything is computed in fp32 and rounded once to bf16.
 //
-// Bound by bytes: 4 x 4096 tokens of 32 + 8 heads of 128 take 60 us (335 MB, 5.6
-// TB/s).  What an SM needs is loads outstanding while other rows are reduced: 32
-// warps with four rows each (64 registers; in blocks of 128 threads, 62 us in
-// blocks of 256).  16 x 1024 tokens of 16 + 16 heads of 64,
-// forward and gradients, take 63 us: 23 + 40, 5.3 TB/s over the five tensors of
-// 67 MB that the two calls read and write.  One token for each of 8 sequences takes 2.4 us.
+// Bound by bytes: 4 x 4096 tokens of 32 + 8 heads of 128 take 54 us (335 MB, 6.2
+// TB/s).  What an SM needs is loads outstanding while other rows are reduced: 28 to
+// 32 warps with four rows each, in small blocks, so that few wait for a block's
+// last (with 128 threads 56 us, and 1 x 4096 tokens 16.5 for 15.1).  16 x 1024 tokens of 16 + 16 heads of 64,
+// forward and gradients, take 63 us: 22 + 41, 5.3 TB/s over the five tensors of
+// 67 MB that the two calls read and write.  One token for each of 8 sequences takes 2.2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,16 +43,20 @@
 namespace tkattn {
 namespace {
 
-constexpr int kNrFwdThreads = 128, kNrBwdThreads = 256;
+constexpr int kNrFwdThreads = 64, kNrBwdThreads = 256;
+// Forward: blocks of an SM.  72 registers hold the paired halves' kernel, in 64 it
+// spills (4 x 4096 tokens, 40 heads of 128: 59.4 us; 65 with 12 blocks); the other fits 64.
+template <bool kHalves>
+constexpr int kNrFwdBlocks = kHalves ? 14 : 16;
 // Backward: blocks of an SM, and heads whose rows are loaded together.  With 16-byte
 // loads (neighbours paired) fewer warps with more rows each are the faster (16 x
 // 1024 tokens, 32 heads of 64, with the forward: 63.3 us, 65.3 the other way),
-// with 8-byte loads more warps (4 x 4096, 40 heads of 128: 153 us, 159).
+// with 8-byte loads more warps (4 x 4096, 40 heads of 128, 6 us more the other way).
 template <bool kHalves>
 constexpr int kNrBwdBlocks = kHalves ? 3 : 2;
 template <bool kHalves>
 constexpr int kNrBwdUnroll = kHalves ? 2 : 4;
-constexpr int kNrFwdHeads = 16, kNrBwdHeads = 8;  // heads a row group takes for one token, at most
+constexpr int kNrFwdHeads = 32, kNrBwdHeads = 8;  // heads a row group takes for one token, at most
 // Rows of partial weight gradients: one for each block of the backward.
 constexpr int kNrBwdMaxBlocks = 2048;
 
@@ -75,6 +79,7 @@ struct NrParams {
   int hpg;          // heads a row group takes for one token
   int chunks[2];    // ceil(H / hpg): gridDim.y of the two together
   int tiles;        // ceil(B * N / groups per block)
+  int early;        // the next grid may begin beside this one (tk_launch.cuh)
   float *dw_part;   // [gridDim.y * gridDim.x, D]: the queries' rows, then the keys'
 };
 
@@ -180,7 +185,7 @@ __device__ __forceinline__ float group_sum(float s) {
 // the queries' first).  A block takes one token for each of its row groups.
 template <int D, bool kHalves, bool kBwd>
 __global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads,
-                                  kBwd ? kNrBwdBlocks<kHalves> : 8)
+                                  kBwd ? kNrBwdBlocks<kHalves> : kNrFwdBlocks<kHalves>)
     tk_norm_rope_kernel(const __grid_constant__ NrParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = (kBwd ? kNrBwdThreads : kNrFwdThreads) / kLanes;
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads,
   const int which = (int)blockIdx.y >= p.chunks[0];
   const int h0 = ((int)blockIdx.y - (which ? p.chunks[0] : 0)) * p.hpg;
   const int h1 = min(h0 + p.hpg, p.H[which]);
-  grid_launch_dependents();
+  grid_launch_dependents_if(p.early);
   grid_wait();
   const NrTensor X = p.x[which];
   const long long yh = p.yh[which];
@@ -542,6 +547,7 @@ extern "C" int tk_attn_qk_norm_rope(
   }
   split(p, D, kNrFwdThreads, kNrFwdHeads, 65535, 16LL * dv.num_sms);
   const dim3 grid(p.tiles, p.chunks[0] + p.chunks[1]);
+  p.early = one_wave((long long)grid.x * grid.y, dv.num_sms);
   return launch<false>(p, D, !interleaved, grid, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? TK_ATTN_OK
@@ -640,6 +646,7 @@ extern "C" int tk_attn_qk_norm_rope_bwd(
   const int blocks = (interleaved ? kNrBwdBlocks<false> : kNrBwdBlocks<true>) * dv.num_sms;
   split(p, D, kNrBwdThreads, kNrBwdHeads, kNrBwdMaxBlocks, blocks);
   p.dw_part = static_cast<float *>(workspace);
+  p.early = 1;
   const int runs = p.chunks[0] + p.chunks[1];
   int cols = blocks / runs;
   cols = cols < 1 ? 1 : cols > p.tiles ? p.tiles : cols;
