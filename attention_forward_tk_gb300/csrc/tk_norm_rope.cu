@@ -25,9 +25,10 @@
 // Bound by bytes: 4 x 4096 tokens of 32 + 8 heads of 128 take 54 us (335 MB, 6.2
 // TB/s).  What an SM needs is loads outstanding while other rows are reduced: 28 to
 // 32 warps with four rows each, in small blocks, so that few wait for a block's
-// last (with 128 threads 56 us, and 1 x 4096 tokens 16.5 for 15.1).  16 x 1024 tokens of 16 + 16 heads of 64,
-// forward and gradients, take 63 us: 22 + 41, 5.3 TB/s over the five tensors of
-// 67 MB that the two calls read and write.  One token for each of 8 sequences takes 2.2 us.
+// last (with 128 threads 56 us, and 1 x 4096 tokens 16.5 for 15.1).  16 x 1024
+// tokens of 16 + 16 heads of 64, forward and gradients, take 61 us: 22 + 39, 5.5
+// TB/s over the five tensors of 67 MB that the two calls read and write.  One token
+// for each of 8 sequences takes 2.2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -48,14 +49,10 @@ constexpr int kNrFwdThreads = 64, kNrBwdThreads = 256;
 // spills (4 x 4096 tokens, 40 heads of 128: 59.4 us; 65 with 12 blocks); the other fits 64.
 template <bool kHalves>
 constexpr int kNrFwdBlocks = kHalves ? 14 : 16;
-// Backward: blocks of an SM, and heads whose rows are loaded together.  With 16-byte
-// loads (neighbours paired) fewer warps with more rows each are the faster (16 x
-// 1024 tokens, 32 heads of 64, with the forward: 63.3 us, 65.3 the other way),
-// with 8-byte loads more warps (4 x 4096, 40 heads of 128, 6 us more the other way).
-template <bool kHalves>
-constexpr int kNrBwdBlocks = kHalves ? 3 : 2;
-template <bool kHalves>
-constexpr int kNrBwdUnroll = kHalves ? 2 : 4;
+// Backward: blocks of an SM, and heads whose rows are loaded together, the next ones
+// while these are worked on (without that 16 x 1024 tokens, 32 heads of 64, took
+// with the forward 62.7 us for 61.3 and four heads at a time on two blocks).
+constexpr int kNrBwdBlocks = 3, kNrBwdUnroll = 2;
 constexpr int kNrFwdHeads = 32, kNrBwdHeads = 8;  // heads a row group takes for one token, at most
 // Rows of partial weight gradients: one for each block of the backward.
 constexpr int kNrBwdMaxBlocks = 2048;
@@ -185,11 +182,11 @@ __device__ __forceinline__ float group_sum(float s) {
 // the queries' first).  A block takes one token for each of its row groups.
 template <int D, bool kHalves, bool kBwd>
 __global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads,
-                                  kBwd ? kNrBwdBlocks<kHalves> : kNrFwdBlocks<kHalves>)
+                                  kBwd ? kNrBwdBlocks : kNrFwdBlocks<kHalves>)
     tk_norm_rope_kernel(const __grid_constant__ NrParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = (kBwd ? kNrBwdThreads : kNrFwdThreads) / kLanes;
-  constexpr int kUnroll = kBwd ? kNrBwdUnroll<kHalves> : 4;  // heads whose rows are loaded together
+  constexpr int kUnroll = kBwd ? kNrBwdUnroll : 4;  // heads whose rows are loaded together
   const int l = threadIdx.x % kLanes;
   const int grp = threadIdx.x / kLanes;
   int lo, hi;
@@ -261,10 +258,10 @@ __global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads,
         yrow += kUnroll * yh;
       }
     } else {
+      // The next heads' rows are on their way while these are worked on.
       const NrTensor G = p.dy[which];
       const __nv_bfloat16 *grow = G.p + b * G.sb + n * G.sn + h0 * G.sh;
-      for (int h = 0; h < h1 - h0; h += kUnroll) {
-        Raw x[kUnroll], y[kUnroll];
+      auto load = [&](Raw(&x)[kUnroll], Raw(&y)[kUnroll], int h) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           x[u].lo = x[u].hi = y[u].lo = y[u].hi = make_uint2(0, 0);
@@ -275,6 +272,8 @@ __global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads,
         }
         xrow += kUnroll * X.sh;
         grow += kUnroll * G.sh;
+      };
+      auto work = [&](const Raw(&x)[kUnroll], const Raw(&y)[kUnroll], int h) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           float a[4], c[4], ga[4], gb[4];
@@ -310,6 +309,15 @@ __global__ void __launch_bounds__(kBwd ? kNrBwdThreads : kNrFwdThreads,
           if (h + u < end) store8<kHalves>(yrow + u * yh, lo, hi, va, vb);
         }
         yrow += kUnroll * yh;
+      };
+      Raw x0[kUnroll], y0[kUnroll], x1[kUnroll], y1[kUnroll];
+      load(x0, y0, 0);
+      for (int h = 0; h < h1 - h0; h += 2 * kUnroll) {
+        load(x1, y1, h + kUnroll);
+        work(x0, y0, h);
+        if (h + kUnroll >= h1 - h0) break;
+        load(x0, y0, h + 2 * kUnroll);
+        work(x1, y1, h + kUnroll);
       }
     }
   }
@@ -643,7 +651,7 @@ extern "C" int tk_attn_qk_norm_rope_bwd(
   p.dy[1] = {static_cast<const __nv_bfloat16 *>(dk_out), dk_out_strides[0], dk_out_strides[1],
              dk_out_strides[2]};
   // As many blocks as are resident at once, each over several tiles.
-  const int blocks = (interleaved ? kNrBwdBlocks<false> : kNrBwdBlocks<true>) * dv.num_sms;
+  const int blocks = kNrBwdBlocks * dv.num_sms;
   split(p, D, kNrBwdThreads, kNrBwdHeads, kNrBwdMaxBlocks, blocks);
   p.dw_part = static_cast<float *>(workspace);
   p.early = 1;
