@@ -15,7 +15,7 @@
 // the exponents a write gives).
 // Both are bound by the bytes they move.  Measured, with 8 heads of 128: up to
 // 4096 tokens written for each of 8 sequences in 18.6 us (114 MB, 6.1 TB/s); one
-// for each of 64 in 3.9 us, most of it the start of a grid and three dependent
+// for each of 64 in 4.0 us, most of it the start of a grid and three dependent
 // reads (position, page, exponent); 8 sequences of up to 16384 positions read
 // back in 72 us (453 MB, 6.3 TB/s).
 // A write's block is a page, not more, because a page's exponent needs all of
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kKv8Threads)
     // rows that stay, onto the new grid
     const float s = exp2i(max(held - e, -126));
     uint2 *old = reinterpret_cast<uint2 *>(page);
-    constexpr int kDeep = kMaxVec < 8 ? kMaxVec : 8;  // reads in flight
+    constexpr int kDeep = kMaxVec < 4 ? kMaxVec : 4;  // reads in flight
 #pragma unroll 1
     for (int c0 = threadIdx.x; c0 < r0 * kVec; c0 += kDeep * kKv8Threads) {
       uint2 w[kDeep];
