@@ -5,10 +5,10 @@
 // programmatic stream serialization: a grid's blocks may become resident while
 // the grid before still runs, and every thread waits (grid_wait) before it
 // reads or writes device memory, for all of that grid to have ended and its
-// writes to be visible.  A grid that was launched the plain way ends before, as ever; and one
-// that calls grid_launch_dependents lets the next begin once all its own blocks
-// have.  Every block waits, whatever it then does: a grid's end so implies the
-// end of all grids before it.
+// writes to be visible.  A grid that was launched the plain way ends before, as
+// ever; and one that calls grid_launch_dependents lets the next begin once all its
+// own blocks have.  Every block waits, whatever it then does: a grid's end so
+// implies the end of all grids before it.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -29,10 +29,10 @@ __device__ __forceinline__ void grid_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Whether a grid's blocks (of 64 or 128 threads) are all resident at once.  One that is
-// not leaves the next alone: where that began beside the last of many waves, its
-// blocks came to lie differently on the SMs (norm with rotation, then its gradients, 4 x
-// 4096 tokens, 40 heads of 128: 166 us, 146 one behind the other).
+// Whether a grid's blocks (of 64 or 128 threads) can all be resident at once.  One
+// that is not leaves the next alone: begun beside the last of many waves, that ran
+// slower than one behind the other (norm with rotation, then its gradients, 4 x 4096
+// tokens, 40 heads of 128: 166 us for 146).
 inline int one_wave(long long blocks, int num_sms) { return blocks <= 16LL * num_sms; }
 
 template <typename... Params, typename... Args>
